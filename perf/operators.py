@@ -236,13 +236,13 @@ def prepare(case, seed):
             if n:
                 k = _signal(g, Hkv, n, d, w).to(dt)
                 v = torch.randn(Hkv, n, d, generator=g, device="cuda").to(dt)
-                _plain_append(k[None], v[None], sigma, pool, table[b:b + 1], [0], [n])
+                _plain_append(k[None], v[None], sigma, pool, table[b:b + 1], _i32([0]), _i32([n]))
         q = _signal(g, Hkv, B * T * (Hq // Hkv), d, w).reshape(Hq, B, T, d).transpose(0, 1)
         return dict(case=case, pool=pool, table=table, lens=_i32(lens), counts=_i32(counts),
                     q=q.to(dt).contiguous(),
                     sigma_q=1.4 + 0.1 * torch.rand(Hq, generator=g, device="cuda"),
                     N=case["N"], tau=1.0 / math.sqrt(d), window=case["window"],
-                    sinks=case["sinks"], own=_own_cache(pool))
+                    sinks=case["sinks"])
     if case["kind"] == "append":
         B, T = case["B"], case["T"]
         dt = DT[case["dtype"]]
@@ -255,8 +255,7 @@ def prepare(case, seed):
         # a few channels of values run larger than the rest, as they do in practice
         v = (v * (1 + 4 * (torch.arange(d, device="cuda") % 23 == 0))).to(dt)
         return dict(case=case, pool=pool, table=table, start=_i32(start), count=_i32(count), k=k,
-                    v=v, sigma_k=0.9 + 0.2 * torch.rand(Hkv, generator=g, device="cuda"),
-                    own=_own_cache(pool))
+                    v=v, sigma_k=0.9 + 0.2 * torch.rand(Hkv, generator=g, device="cuda"))
     S = case["S"]
     lens = _lengths(case, S)
     width = _ceil(case["len_max"], page) + 2
@@ -268,7 +267,7 @@ def prepare(case, seed):
         raw.copy_(torch.randint(-2 ** 31, 2 ** 31, raw.shape, generator=g, device="cuda"))
         if a.dtype == torch.bfloat16:
             a.copy_(torch.rand(a.shape, generator=g, device="cuda"))
-    st = dict(case=case, pool=pool, table=table, refs=refs, lens=_i32(lens), own=_own_cache(pool))
+    st = dict(case=case, pool=pool, table=table, refs=refs, lens=_i32(lens))
     if case["kind"] == "copy":
         free = torch.nonzero(refs == 0).flatten()
         used = torch.nonzero(refs).flatten()
@@ -290,19 +289,18 @@ def prepare(case, seed):
     return st
 
 
-def _own_cache(pool):
-    if not own:
-        return None
-    from sparse_attention_sigma_b200 import cache
-    return cache.Cache(*pool.arrays())
-
-
 # ------------------------------------------------------------------ plain forms
 
 def _slots(pool, table, b, pos):
-    """Page and slot of positions `pos` of the sequence of table row b."""
+    """Page and slot of positions `pos` of the sequences of table rows b."""
     page = pool.kbits.shape[2]
-    return table[b].long()[pos // page], pos % page
+    return table[b, pos // page].long(), pos % page
+
+
+def _new_tokens(start, count, T):
+    """Sequence, index and position of every new token of a padded batch, as flat lists."""
+    b, t = torch.nonzero(torch.arange(T, device="cuda") < count[:, None], as_tuple=True)
+    return b, t, start[b] + t
 
 
 def _bits(neg):
@@ -334,23 +332,20 @@ def _plain_quantise(v):
 
 def _plain_append(k, v, sigma, pool, table, start, count):
     neg = (k.float() / sigma[None, :, None, None]) < 0
-    for b, (s, c) in enumerate(zip(start, count)):
-        if c == 0:
-            continue
-        p, slot = _slots(pool, table, b, torch.arange(s, s + c, device="cuda"))
-        code, scale, zero = _plain_quantise(v[b, :, :c])
-        byte = (code[..., 0::2] + 16 * code[..., 1::2]).to(torch.uint8)
-        pool.kbits[p, :, slot] = _bits(neg[b, :, :c]).transpose(0, 1)
-        pool.vcodes[p, :, slot] = byte.transpose(0, 1)
-        pool.vscale[p, :, slot] = torch.stack([scale, zero], -1).to(torch.bfloat16).transpose(0, 1)
+    b, t, pos = _new_tokens(start, count, k.shape[2])
+    p, slot = _slots(pool, table, b, pos)
+    code, scale, zero = _plain_quantise(v[b, :, t])
+    pool.kbits[p, :, slot] = _bits(neg[b, :, t])
+    pool.vcodes[p, :, slot] = (code[..., 0::2] + 16 * code[..., 1::2]).to(torch.uint8)
+    pool.vscale[p, :, slot] = torch.stack([scale, zero], -1).to(torch.bfloat16)
 
 
 def _plain_values(pool, p, slot):
-    """Values of cached tokens, fp32 [heads, tokens, d]."""
-    byte = pool.vcodes[p, :, slot].to(torch.int32)
+    """Values of cached tokens, fp32 [..., heads, d] for pages and slots [...]."""
+    byte = pool.vcodes[p, :, slot]
     code = torch.stack([byte & 15, byte >> 4], -1).flatten(-2)
     sz = pool.vscale[p, :, slot].float()
-    return (code * sz[..., :1] + sz[..., 1:]).transpose(0, 1)
+    return code * sz[..., :1] + sz[..., 1:]
 
 
 def _plain_read(pool, table, start, count, T):
@@ -358,49 +353,46 @@ def _plain_read(pool, table, start, count, T):
     B = table.shape[0]
     bits = torch.zeros(B, H, T, d // 32, dtype=torch.int32, device="cuda")
     vals = torch.zeros(B, H, T, d, device="cuda")
-    for b, (s, c) in enumerate(zip(start, count)):
-        p, slot = _slots(pool, table, b, torch.arange(s, s + c, device="cuda"))
-        bits[b, :, :c] = pool.kbits[p, :, slot].transpose(0, 1)
-        vals[b, :, :c] = _plain_values(pool, p, slot)
+    b, t, pos = _new_tokens(start, count, T)
+    p, slot = _slots(pool, table, b, pos)
+    bits[b, :, t] = pool.kbits[p, :, slot]
+    vals[b, :, t] = _plain_values(pool, p, slot)
     return bits, vals
 
 
-def _visible(pos, L, window, sinks):
-    j = torch.arange(L, device="cuda")[None]
-    vis = j <= pos[:, None]
-    if window > 0:
-        vis &= (j > pos[:, None] - window) | (j < sinks)
-    return vis
-
-
 def _plain_attend(st):
-    pool, table, q = st["pool"], st["table"], st["q"]
+    pool, table, q, lens = st["pool"], st["table"], st["q"], st["lens"].long()
     B, Hq, T, d = q.shape
     Hkv = pool.kbits.shape[1]
     G = Hq // Hkv
-    out = torch.zeros(B, Hq, T, d, device="cuda")
+    L = table.shape[1] * pool.kbits.shape[2]
+    j = torch.arange(L, device="cuda")
+    p, slot = _slots(pool, table.clamp(min=0), torch.arange(B, device="cuda")[:, None],
+                     j.expand(B, L))
+    word = pool.kbits[p, :, slot].transpose(1, 2)
+    sk = 1.0 - 2.0 * ((word[..., None] >> torch.arange(32, device="cuda")) & 1).flatten(-2)
     sq = 1.0 - 2.0 * ((q.float() / st["sigma_q"][None, :, None, None]) < 0).float()
-    for b, (L, c) in enumerate(zip(st["lens"].tolist(), st["counts"].tolist())):
-        if L == 0 or c == 0:
-            continue
-        p, slot = _slots(pool, table, b, torch.arange(L, device="cuda"))
-        word = pool.kbits[p, :, slot].transpose(0, 1)
-        sk = 1.0 - 2.0 * ((word[..., None] >> torch.arange(32, device="cuda")) & 1).flatten(-2)
-        s = sq[b, :, :c].reshape(Hkv, G * c, d) @ sk.transpose(1, 2)
-        vis = _visible(torch.arange(L - c, L, device="cuda"), L, st["window"], st["sinks"])
-        vis = vis.repeat(G, 1)[None]
-        h = torch.where(vis, (d - s) * 0.5, torch.full_like(s, d + 1)).to(torch.int16)
-        n = vis.sum(-1, keepdim=True).clamp(max=st["N"])
-        t = h.sort(-1).values.gather(-1, (n.long() - 1).clamp(min=0).expand(Hkv, -1, 1))
-        less = vis & (h < t)
-        tie = vis & (h == t)
-        keep = less | (tie & (tie.cumsum(-1) <= n - less.sum(-1, keepdim=True)))
-        best = torch.where(vis, s, torch.full_like(s, -float(d))).amax(-1, keepdim=True)
-        w = torch.exp(st["tau"] * (s - best)) * keep
-        z = w.sum(-1, keepdim=True)
-        o = (w @ _plain_values(pool, p, slot)) / torch.where(z > 0, z, torch.ones_like(z))
-        out[b, :, :c] = o.reshape(Hq, c, d)
-    return out
+    s = sq.reshape(B, Hkv, G * T, d) @ sk.transpose(2, 3)
+    # position of token t of a sequence; tokens past its count see nothing
+    t = torch.arange(T, device="cuda")
+    pos = torch.where(t < st["counts"][:, None], (lens - st["counts"])[:, None] + t, -1)[..., None]
+    vis = j <= pos
+    if st["window"] > 0:
+        vis &= (j > pos - st["window"]) | (j < st["sinks"])
+    vis = vis.repeat(1, G, 1)[:, None]
+    h = torch.where(vis, (d - s) * 0.5, d + 1.0).to(torch.uint8)
+    n = vis.sum(-1, keepdim=True).clamp(max=st["N"])
+    last = h.sort(-1).values.gather(-1, (n - 1).clamp(min=0).expand(B, Hkv, G * T, 1))
+    less = vis & (h < last)
+    tie = vis & (h == last)
+    keep = less | (tie & (tie.cumsum(-1) <= n - less.sum(-1, keepdim=True)))
+    best = torch.where(vis, s, -float(d)).amax(-1, keepdim=True)
+    w = torch.exp(st["tau"] * (s - best)) * keep
+    z = w.sum(-1, keepdim=True)
+    # pages behind a sequence hold what earlier tokens left: their weights are 0, their values cut
+    seen = (j < lens[:, None])[..., None, None]
+    value = torch.where(seen, _plain_values(pool, p, slot), 0.0).transpose(1, 2)
+    return ((w @ value) / torch.where(z > 0, z, 1.0)).reshape(B, Hq, T, d)
 
 
 def _plain_fork(table, lens, refs, src, dst):
@@ -486,9 +478,8 @@ def run(st):
     if case["kind"] == "attend":
         return _plain_attend(st)
     if case["kind"] == "append":
-        start, count = st["start"].tolist(), st["count"].tolist()
-        _plain_append(st["k"], st["v"], st["sigma_k"], pool, st["table"], start, count)
-        return _plain_read(pool, st["table"], start, count, case["T"])
+        _plain_append(st["k"], st["v"], st["sigma_k"], pool, st["table"], st["start"], st["count"])
+        return _plain_read(pool, st["table"], st["start"], st["count"], case["T"])
     if case["kind"] == "copy":
         _plain_copy(pool, st["src"], st["dst"])
         return pool.raw()
@@ -508,7 +499,7 @@ def run(st):
 
 def _run_own(st):
     from sparse_attention_sigma_b200 import cache
-    case, pool = st["case"], st["own"]
+    case, pool = st["case"], cache.Cache(*st["pool"].arrays())
     if case["kind"] == "attend":
         return cache.had_cache_attention(st["q"], st["sigma_q"], pool, st["table"], st["lens"],
                                          st["N"], st["tau"], window=st["window"],
