@@ -395,17 +395,19 @@ def _plain_attend(st):
     return ((w @ value) / torch.where(z > 0, z, 1.0)).reshape(B, Hq, T, d)
 
 
-def _plain_fork(table, lens, refs, src, dst):
+def _plain_fork(table, lens, refs, page, src, dst):
     s, t = src.long(), dst.long()
-    new, old = table[s], table[t]
-    new_len = lens[s]
+    new_len, old = lens[s], table[t]
+    # pages that were reserved behind the source's tokens stay the source's own
+    held = torch.arange(table.shape[1], device="cuda")[None] * page < new_len[:, None]
+    new = torch.where(held, table[s], -1)
     refs.index_add_(0, new[new >= 0].long(), torch.ones_like(new[new >= 0]))
     refs.index_add_(0, old[old >= 0].long(), -torch.ones_like(old[old >= 0]))
     table[t] = new
     lens[t] = new_len
 
 
-def _plain_reserve(table, lens, refs, grow, page):
+def _plain_reserve(table, lens, refs, page, grow):
     S, width = table.shape
     have = (lens + page - 1) // page
     want = torch.where(grow > 0, (lens + grow + page - 1) // page, have)
@@ -415,7 +417,8 @@ def _plain_reserve(table, lens, refs, grow, page):
     earlier = ((shared[None] == shared[:, None]) & part[None]).tril(-1).sum(1)
     copy = part & (refs[shared.clamp(min=0).long()] - earlier > 1)
     idx = torch.arange(width, device="cuda")[None]
-    need = ((idx >= have[:, None]) & (idx < want[:, None])) | (copy[:, None] & (idx == last[:, None]))
+    need = (idx >= have[:, None]) & (idx < want[:, None]) & (table < 0)
+    need |= copy[:, None] & (idx == last[:, None])
     where = torch.nonzero(need)
     page_of = torch.nonzero(refs == 0).flatten()[:where.shape[0]].to(torch.int32)
     refs[page_of.long()] = 1
@@ -485,8 +488,8 @@ def run(st):
         return pool.raw()
     table, lens, refs = st["table"].clone(), st["lens"].clone(), st["refs"].clone()
     if case["kind"] == "beam":
-        _plain_fork(table, lens, refs, st["src"], st["dst"])
-        src, dst = _plain_reserve(table, lens, refs, st["grow"], case["page"])
+        _plain_fork(table, lens, refs, case["page"], st["src"], st["dst"])
+        src, dst = _plain_reserve(table, lens, refs, case["page"], st["grow"])
         _plain_copy(pool, src, dst)
         if case["window"] > 0:
             _plain_evict(table, lens, refs, case["page"], case["window"], case["sinks"])
@@ -513,13 +516,13 @@ def _run_own(st):
         return st["pool"].raw()
     table, lens, refs = st["table"].clone(), st["lens"].clone(), st["refs"].clone()
     if case["kind"] == "beam":
-        cache.had_cache_fork(table, lens, refs, st["src"], st["dst"])
-        src, dst = cache.had_cache_reserve(table, lens, refs, st["grow"], case["page"])
+        cache.had_cache_fork(table, lens, refs, case["page"], st["src"], st["dst"])
+        src, dst = cache.had_cache_reserve(table, lens, refs, case["page"], st["grow"])
         cache.had_cache_copy_pages(pool, src, dst)
         if case["window"] > 0:
             cache.had_cache_evict(table, lens, refs, case["page"], case["window"], case["sinks"])
         return (table, lens, refs, src, dst) + st["pool"].raw()
-    cache.had_cache_free(table, lens, refs, case["page"], st["leave"])
+    cache.had_cache_free(table, lens, refs, st["leave"])
     src, dst, live = cache.had_cache_compact(table, refs)
     cache.had_cache_copy_pages(pool, src, dst)
     return (table, lens, refs, src, dst, live) + st["pool"].raw()
