@@ -25,6 +25,10 @@
  *     (had_soft_attention_fwd; had_soft_binarize, had_soft_topn,
  *     had_soft_softmax_av);
  *   - the straight-through backward (had_attention_bwd);
+ *   - the decoder cache: attention of new tokens to it (had_cache_attention),
+ *     writing and reading tokens (had_cache_append, had_cache_read), and its
+ *     pages' books (had_cache_fork, _reserve, _free, _evict, _compact,
+ *     _copy_pages);
  *   - had_workspace_bytes, had_launch_count, had_status_string,
  *     had_set_wait_limit_ns.
  *
@@ -74,7 +78,8 @@ typedef enum {
     HAD_ERR_WORKSPACE = 3,    /* workspace null or smaller than had_workspace_bytes() */
     HAD_ERR_CUDA = 4,         /* a CUDA launch or runtime call failed */
     HAD_ERR_BAD_SIGMA = 5,    /* device flag: a sigma is <= 0, NaN or infinite */
-    HAD_ERR_TIMEOUT = 6       /* device flag: a bounded on-chip wait gave up */
+    HAD_ERR_TIMEOUT = 6,      /* device flag: a bounded on-chip wait gave up */
+    HAD_ERR_NO_PAGES = 7      /* device flag: the pool has too few free pages */
 } had_status_t;
 
 typedef enum {
@@ -95,7 +100,16 @@ typedef enum {
     HAD_OP_SOFT_TOPN = 9,         /* had_soft_topn */
     HAD_OP_SOFT_SOFTMAX_AV = 10,  /* had_soft_softmax_av */
     HAD_OP_SOFT_ATTENTION_FWD = 11, /* had_soft_attention_fwd */
-    HAD_OP_ATTENTION_BWD = 12     /* had_attention_bwd */
+    HAD_OP_ATTENTION_BWD = 12,    /* had_attention_bwd */
+    HAD_OP_CACHE_ATTENTION = 13,  /* had_cache_attention */
+    HAD_OP_CACHE_APPEND = 14,     /* had_cache_append */
+    HAD_OP_CACHE_READ = 15,       /* had_cache_read */
+    HAD_OP_CACHE_FORK = 16,       /* had_cache_fork */
+    HAD_OP_CACHE_RESERVE = 17,    /* had_cache_reserve */
+    HAD_OP_CACHE_FREE = 18,       /* had_cache_free */
+    HAD_OP_CACHE_EVICT = 19,      /* had_cache_evict */
+    HAD_OP_CACHE_COMPACT = 20,    /* had_cache_compact */
+    HAD_OP_CACHE_COPY_PAGES = 21  /* had_cache_copy_pages */
 } had_op_t;
 
 /*
@@ -365,6 +379,167 @@ HAD_API had_status_t had_attention_fwd_noalloc(const void *Q, const void *K, con
 
 /* Size in bytes of the fixed array had_attention_fwd_noalloc works in. */
 HAD_API size_t had_noalloc_scratch_bytes(void);
+
+/*
+ * The decoder cache.
+ *
+ * A binarized key is read only through its sign, so the cache holds d bits
+ * per key, exactly; a value is held in 4 bits per element with a scale s and
+ * a zero point z (both bf16) per token and head, and stands for c s + z.  At
+ * d = 128 a token and head take 84 bytes instead of the 512 of bf16 K and V.
+ * Tokens lie in pages of `page` tokens; a sequence's pages are listed in its
+ * row of a table, so that sequences of a beam share their common part.
+ *
+ *   had_cache_t (a host struct, read during the call) names the pool:
+ *     kbits   [pages, heads, page, d/32] uint32 (device), packed as above
+ *     vcodes  [pages, heads, page, d/2] uint8: element 2i of the value in the
+ *             low nibble of byte i, element 2i + 1 in the high one
+ *     vscale  [pages, heads, page, 2] bf16: s, then z
+ *     page    16, 32, 64, 128 or 256;  d 64 or 128
+ *   table   [S, max_pages] int32 (device): pages of sequence s in order, -1
+ *           for none.  max_pages * page < 2^31.
+ *   lens    [S] int32: tokens of a sequence;  refs [pages] int32: how many
+ *           table entries name a page, 0 = free.  The caller starts them with
+ *           -1, 0 and 0.
+ * table, lens, refs, index and count arrays need 4-byte alignment only.
+ * A table entry outside [0, pages), -1 included, where a call needs a page
+ * flags HAD_ERR_INVALID_ARG and the token is skipped.  No call uses a
+ * workspace, and all may be captured into a graph.  Calls that share a pool
+ * or books and overlap on the GPU race, as on any buffer that one of them
+ * writes.
+ */
+typedef struct {
+    uint32_t *kbits;
+    uint8_t *vcodes;
+    void *vscale;
+    int pages, heads, page, d;
+} had_cache_t;
+
+/*
+ * Tokens into the cache: token t of sequence b goes to position start[b] + t.
+ *   K, V    [B, heads, T, d] of dtype dt (device); sigma_k [heads] float
+ *   table   [B, max_pages]; start [B] int32; counts [B] int32 or NULL: how
+ *           many of the T tokens are real (NULL: all)
+ * Signs as had_binarize_pack.  Values, every step in IEEE fp32: z = the row's
+ * minimum rounded down to bf16, s = fl(fl(max - z) / 15) rounded up to bf16,
+ * c = fl(fl(v - z) / s) rounded to the nearest whole number, ties to even,
+ * clamped to [0, 15]; s = 0 gives c = 0.  |c s + z - v| <= s / 2 plus fp32
+ * rounding.  A row with a NaN or an infinity, or whose z or 15 s is not
+ * finite, gets s = z = NaN.  The pages have to be there and the sequence's own
+ * (had_cache_reserve); places behind the written tokens are left as they were.
+ */
+HAD_API had_status_t had_cache_append(const void *K, const void *V, had_dtype_t dt,
+                                      const float *sigma_k, const had_cache_t *cache,
+                                      const int32_t *table, int max_pages, const int32_t *start,
+                                      const int32_t *counts, int B, int T, int32_t *dev_status,
+                                      cudaStream_t stream);
+
+/*
+ * Tokens of the cache: bits [B, heads, T, d/32] uint32 and values
+ * [B, heads, T, d] float, fl(c s + z), of positions start[b] .. start[b] +
+ * counts[b] - 1; zeros behind them.  Either output may be NULL.
+ */
+HAD_API had_status_t had_cache_read(const had_cache_t *cache, const int32_t *table, int max_pages,
+                                    const int32_t *start, const int32_t *counts, int B, int T,
+                                    uint32_t *bits, float *values, int32_t *dev_status,
+                                    cudaStream_t stream);
+
+/*
+ * Attention of the newest tokens of each sequence to the cache (which holds
+ * them already): one token while generating, several of a draft, or a chunk
+ * of a prompt.
+ *   Q       [B, Hq, T, d] of dtype dt; Hq a multiple of heads: query head hq
+ *           reads key-value head hq / (Hq / heads); sigma_q [Hq] float
+ *   lens    [B] tokens in the cache; counts [B] or NULL: how many of the T
+ *           query tokens are real, the last of them at position lens - 1
+ *   N       >= 1: kept keys per row; a row with fewer visible keys keeps all
+ *   window  0, or W >= 1: position i sees j <= i with j > i - W or j < sinks
+ *   sinks   >= 0: first tokens that stay visible under a window
+ *   out     [B, Hq, T, d] float
+ * The rule of had_attention_causal_fwd at position i = lens[b] - counts[b] +
+ * t, over the cached signs and values.  Rows at or behind counts[b], at a
+ * negative position, or of an empty sequence are zeros.  A row that keeps a
+ * token with a NaN scale is NaN.
+ */
+HAD_API had_status_t had_cache_attention(const void *Q, had_dtype_t dt, const float *sigma_q,
+                                         const had_cache_t *cache, const int32_t *table,
+                                         int max_pages, const int32_t *lens,
+                                         const int32_t *counts, int B, int Hq, int T, int N,
+                                         float tau, int window, int sinks, float *out,
+                                         int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * Forking: sequence dst[i] lets its pages go and continues as a copy of
+ * sequence src[i], sharing the pages of its tokens; all n pairs at once, so a
+ * source may be another pair's destination.  src, dst [n] int32 (device).
+ * An index outside [0, S), a destination listed twice or a length outside
+ * [0, max_pages * page] flags HAD_ERR_INVALID_ARG and changes nothing.
+ * S <= 8192 and n <= S (else HAD_ERR_UNSUPPORTED, HAD_ERR_INVALID_ARG).
+ */
+HAD_API had_status_t had_cache_fork(int32_t *table, int32_t *lens, int32_t *refs, int S,
+                                    int max_pages, int pages, int page, const int32_t *src,
+                                    const int32_t *dst, int n, int32_t *dev_status,
+                                    cudaStream_t stream);
+
+/*
+ * Room for grow[s] more tokens behind the lens[s] of every sequence, in pages
+ * of its own: free pages, in ascending order, for ascending (sequence,
+ * entry).  A last page that is partly filled and shared is exchanged for a
+ * fresh one, src[s] -> dst[s] naming the copy that had_cache_copy_pages then
+ * makes (-1: none); of the growing sequences that share it the last one keeps
+ * it if no other holds it.  Pages reserved by an earlier call and not used
+ * yet are kept.  lens is not changed.
+ *   grow    [S] int32, >= 0;  src, dst [S] int32 out
+ * Too few free pages flags HAD_ERR_NO_PAGES; a grow < 0, more than
+ * max_pages * page tokens, or a table that lacks the last page flags
+ * HAD_ERR_INVALID_ARG.  Either changes nothing and fills src and dst with -1.
+ * S <= 8192.
+ */
+HAD_API had_status_t had_cache_reserve(int32_t *table, const int32_t *lens, int32_t *refs, int S,
+                                       int max_pages, int pages, int page, const int32_t *grow,
+                                       int32_t *src, int32_t *dst, int32_t *dev_status,
+                                       cudaStream_t stream);
+
+/*
+ * The n listed sequences let all their pages go and become empty.  An index
+ * outside [0, S) flags HAD_ERR_INVALID_ARG and is skipped; one listed twice
+ * counts once.
+ */
+HAD_API had_status_t had_cache_free(int32_t *table, int32_t *lens, int32_t *refs, int S,
+                                    int max_pages, int pages, const int32_t *seqs, int n,
+                                    int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * Every sequence lets go of the pages that hold only positions in
+ * [sinks, lens - window): the ones that no query at or behind position
+ * lens - 1 sees under the window.  Their entries become -1, lens stays.
+ */
+HAD_API had_status_t had_cache_evict(int32_t *table, const int32_t *lens, int32_t *refs, int S,
+                                     int max_pages, int pages, int page, int window, int sinks,
+                                     int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * Closes the holes of a pool: with L pages in use, the k-th used page at or
+ * beyond L moves into the k-th free page below L.  table and refs are
+ * renamed; src[k] -> dst[k] ([pages] int32 out, -1 behind the moves) are the
+ * copies that had_cache_copy_pages then makes, live[0] = L.  An entry that
+ * names a free page at or beyond L, or none of the pool's, flags
+ * HAD_ERR_INVALID_ARG and stays.
+ */
+HAD_API had_status_t had_cache_compact(int32_t *table, int32_t *refs, int S, int max_pages,
+                                       int pages, int32_t *src, int32_t *dst, int32_t *live,
+                                       int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * Copies whole pages within a pool: src[i] -> dst[i], n pairs in no order; a
+ * pair with a negative index is skipped, one with an index >= pages flags
+ * HAD_ERR_INVALID_ARG.  A source may be listed twice; the contents of a page
+ * that is a destination twice, or both source and destination, are
+ * unspecified.
+ */
+HAD_API had_status_t had_cache_copy_pages(const had_cache_t *cache, const int32_t *src,
+                                          const int32_t *dst, int n, int32_t *dev_status,
+                                          cudaStream_t stream);
 
 /*
  * Limit, in nanoseconds, of every on-chip wait of the fused forward kernels

@@ -7,14 +7,19 @@ purpose: the standardize step relies on IEEE division with subnormals.
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libhad.so")
-SOURCES = ["had_api.cu"]
+SOURCES = ["had_api.cu", "had_cache.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
+
+
+FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler",
+         "-fvisibility=hidden", "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
 
 
 def _newest_input():
@@ -27,13 +32,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if (not force and os.path.exists(LIB)
             and os.path.getmtime(LIB) >= _newest_input()):
         return LIB
-    cmd = (["nvcc"] + ARCH +
-           ["-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-            "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",
-            "-I", INCLUDE, "-I", CSRC, "-o", LIB + ".tmp"] +
-           (["-Xptxas", "-v"] if verbose else []) +
-           [os.path.join(CSRC, s) for s in SOURCES])
-    subprocess.run(cmd, check=True)
+    # one compiler per source, side by side, then the link
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, s + ".o") for s in SOURCES]
+        jobs = [subprocess.Popen(["nvcc"] + ARCH + FLAGS + (["-Xptxas", "-v"] if verbose else []) +
+                                 ["-c", os.path.join(CSRC, s), "-o", o])
+                for s, o in zip(SOURCES, objects)]
+        codes = [j.wait() for j in jobs]
+        if any(codes):
+            raise subprocess.CalledProcessError(next(c for c in codes if c), "nvcc")
+        subprocess.run(["nvcc"] + ARCH + ["-shared", "-o", LIB + ".tmp"] + objects, check=True)
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

@@ -784,6 +784,16 @@ size_t had_workspace_bytes(int op, int B, int H, int n, int d, int N)
     case HAD_OP_ATTENTION_BWD:
         return check_topn(B, H, n, d, N) == HAD_OK ? bwd_layout(B, H, n, d, N).total
                                                    : (size_t)-1;
+    case HAD_OP_CACHE_ATTENTION:
+    case HAD_OP_CACHE_APPEND:
+    case HAD_OP_CACHE_READ:
+    case HAD_OP_CACHE_FORK:
+    case HAD_OP_CACHE_RESERVE:
+    case HAD_OP_CACHE_FREE:
+    case HAD_OP_CACHE_EVICT:
+    case HAD_OP_CACHE_COMPACT:
+    case HAD_OP_CACHE_COPY_PAGES:
+        return 0;                          // one launch each, in no workspace
     default:
         return (size_t)-1;
     }
@@ -817,6 +827,16 @@ int had_launch_count(int op, int B, int H, int n, int d, int N)
         return check_soft(B, H, n, d, N) == HAD_OK ? 3 + 2 * soft_passes(B, H, n) : -1;
     case HAD_OP_ATTENTION_BWD:
         return check_topn(B, H, n, d, N) == HAD_OK ? 8 : -1;
+    case HAD_OP_CACHE_ATTENTION:
+    case HAD_OP_CACHE_APPEND:
+    case HAD_OP_CACHE_READ:
+    case HAD_OP_CACHE_FORK:
+    case HAD_OP_CACHE_RESERVE:
+    case HAD_OP_CACHE_FREE:
+    case HAD_OP_CACHE_EVICT:
+    case HAD_OP_CACHE_COMPACT:
+    case HAD_OP_CACHE_COPY_PAGES:
+        return 1;
     default:
         return -1;
     }
@@ -832,6 +852,7 @@ const char *had_status_string(had_status_t status)
     case HAD_ERR_CUDA: return "HAD_ERR_CUDA";
     case HAD_ERR_BAD_SIGMA: return "HAD_ERR_BAD_SIGMA";
     case HAD_ERR_TIMEOUT: return "HAD_ERR_TIMEOUT";
+    case HAD_ERR_NO_PAGES: return "HAD_ERR_NO_PAGES";
     }
     return "HAD_ERR_UNKNOWN";
 }

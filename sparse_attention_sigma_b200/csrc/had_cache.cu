@@ -1,0 +1,312 @@
+// had_cache.cu -- the decoder cache's part of the C ABI of include/had.h:
+// argument checks and kernel launches.
+#include <climits>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "had.h"
+#include "had_cache.cuh"
+#include "had_cache_attn.cuh"
+#include "had_cache_pages.cuh"
+
+namespace {
+
+using had::Books;
+using had::CacheView;
+
+constexpr int kMaxSmem = 227 * 1024;   // dynamic shared memory a CTA may have
+
+bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// A required array: there, and aligned.
+bool good(const void *p, size_t to) { return p && aligned(p, to); }
+
+had_status_t launched()
+{
+    return cudaGetLastError() == cudaSuccess ? HAD_OK : HAD_ERR_CUDA;
+}
+
+bool good_page(int page)
+{
+    return page == 16 || page == 32 || page == 64 || page == 128 || page == 256;
+}
+
+int log2_of(int page)
+{
+    int l = 0;
+    while ((1 << l) < page) ++l;
+    return l;
+}
+
+had_status_t check_cache(const had_cache_t *c, CacheView *view)
+{
+    if (!c || c->pages < 1 || c->heads < 1 || c->d < 1) return HAD_ERR_INVALID_ARG;
+    if (c->d != 64 && c->d != 128) return HAD_ERR_UNSUPPORTED;
+    if (!good_page(c->page)) return HAD_ERR_UNSUPPORTED;
+    // rows and bytes of the pool stay far inside 64 bits
+    if ((long long)c->pages * c->heads > (1LL << 40) / c->page) return HAD_ERR_UNSUPPORTED;
+    if (!good(c->kbits, 16) || !good(c->vcodes, 16) || !good(c->vscale, 16))
+        return HAD_ERR_INVALID_ARG;
+    view->kbits = c->kbits;
+    view->vcodes = c->vcodes;
+    view->vscale = static_cast<uint32_t *>(c->vscale);
+    view->pages = c->pages;
+    view->heads = c->heads;
+    view->page_log = log2_of(c->page);
+    return HAD_OK;
+}
+
+had_status_t check_table(const int32_t *table, int rows, int max_pages, int page)
+{
+    if (rows < 1 || max_pages < 1 || !good(table, 4)) return HAD_ERR_INVALID_ARG;
+    return (long long)max_pages * page > INT_MAX ? HAD_ERR_UNSUPPORTED : HAD_OK;
+}
+
+// The books of the page operators; `page` of 1 where a call has none.
+had_status_t check_books(int32_t *table, const int32_t *lens, int32_t *refs, int S, int max_pages,
+                         int pages, int page, Books *books)
+{
+    if (pages < 1 || !good(lens, 4) || !good(refs, 4)) return HAD_ERR_INVALID_ARG;
+    if (page != 1 && !good_page(page)) return HAD_ERR_UNSUPPORTED;
+    const had_status_t s = check_table(table, S, max_pages, page);
+    *books = Books{table, const_cast<int32_t *>(lens), refs, S, max_pages, pages, log2_of(page)};
+    return s;
+}
+
+// A launch of one cluster of the page operators.
+template <typename... Params, typename... Args>
+had_status_t launch_cluster(void (*kernel)(Params...), size_t smem, cudaStream_t st, Args... args)
+{
+    // Set on every call: the attribute belongs to the current device.
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+            cudaSuccess)
+        return HAD_ERR_CUDA;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {had::kBookCtas, 1, 1};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(had::kBookCtas);
+    cfg.blockDim = dim3(had::kBookThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+    return e == cudaSuccess ? launched() : HAD_ERR_CUDA;
+}
+
+unsigned grid_for(long long items, int per_block)
+{
+    const long long blocks = (items + per_block - 1) / per_block, cap = 148LL * 8;
+    return (unsigned)(blocks < cap ? blocks : cap);
+}
+
+template <typename T>
+void launch_append(const void *K, const void *V, const float *sigma, const CacheView &c, int d,
+                   const int32_t *table, int max_pages, const int32_t *start,
+                   const int32_t *counts, int T_, unsigned rows, int32_t *status, cudaStream_t st)
+{
+    const auto *k = static_cast<const T *>(K), *v = static_cast<const T *>(V);
+    const unsigned grid = (rows + 15) / 16;
+    if (d == 64)
+        had::cache_append_kernel<T, 64><<<grid, 256, 0, st>>>(k, v, sigma, c, table, max_pages,
+                                                              start, counts, T_, rows, status);
+    else
+        had::cache_append_kernel<T, 128><<<grid, 256, 0, st>>>(k, v, sigma, c, table, max_pages,
+                                                               start, counts, T_, rows, status);
+}
+
+// Rows (b, head, token) of an append or a read: one 16-lane group each.
+had_status_t check_rows(int B, int heads, int T, unsigned *rows)
+{
+    if (B < 1 || T < 1) return HAD_ERR_INVALID_ARG;
+    const long long bh = (long long)B * heads;
+    if (bh > INT_MAX || bh * T > INT_MAX) return HAD_ERR_UNSUPPORTED;
+    *rows = (unsigned)(bh * T);
+    return HAD_OK;
+}
+
+bool finite_nonneg(float x) { return x >= 0.0f && x <= 3.4028234e38f; }
+
+}  // namespace
+
+extern "C" {
+
+had_status_t had_cache_append(const void *K, const void *V, had_dtype_t dt, const float *sigma_k,
+                              const had_cache_t *cache, const int32_t *table, int max_pages,
+                              const int32_t *start, const int32_t *counts, int B, int T,
+                              int32_t *dev_status, cudaStream_t stream)
+{
+    CacheView c;
+    unsigned rows;
+    had_status_t s = check_cache(cache, &c);
+    if (s == HAD_OK) s = check_rows(B, c.heads, T, &rows);
+    if (s == HAD_OK) s = check_table(table, B, max_pages, cache->page);
+    if (s != HAD_OK) return s;
+    if (dt != HAD_BF16 && dt != HAD_F32) return HAD_ERR_INVALID_ARG;
+    if (!good(K, 16) || !good(V, 16) || !good(sigma_k, 4) || !good(start, 4) ||
+        !aligned(counts, 4) || !aligned(dev_status, 4))
+        return HAD_ERR_INVALID_ARG;
+    if (dt == HAD_BF16)
+        launch_append<__nv_bfloat16>(K, V, sigma_k, c, cache->d, table, max_pages, start, counts, T,
+                                     rows, dev_status, stream);
+    else
+        launch_append<float>(K, V, sigma_k, c, cache->d, table, max_pages, start, counts, T, rows,
+                             dev_status, stream);
+    return launched();
+}
+
+had_status_t had_cache_read(const had_cache_t *cache, const int32_t *table, int max_pages,
+                            const int32_t *start, const int32_t *counts, int B, int T,
+                            uint32_t *bits, float *values, int32_t *dev_status,
+                            cudaStream_t stream)
+{
+    CacheView c;
+    unsigned rows;
+    had_status_t s = check_cache(cache, &c);
+    if (s == HAD_OK) s = check_rows(B, c.heads, T, &rows);
+    if (s == HAD_OK) s = check_table(table, B, max_pages, cache->page);
+    if (s != HAD_OK) return s;
+    if (!good(start, 4) || !aligned(counts, 4) || !aligned(bits, 16) || !aligned(values, 16) ||
+        !aligned(dev_status, 4))
+        return HAD_ERR_INVALID_ARG;
+    if (!bits && !values) return HAD_ERR_INVALID_ARG;
+    const unsigned grid = (rows + 15) / 16;
+    if (cache->d == 64)
+        had::cache_read_kernel<64><<<grid, 256, 0, stream>>>(c, table, max_pages, start, counts, T,
+                                                             rows, bits, values, dev_status);
+    else
+        had::cache_read_kernel<128><<<grid, 256, 0, stream>>>(c, table, max_pages, start, counts, T,
+                                                              rows, bits, values, dev_status);
+    return launched();
+}
+
+had_status_t had_cache_attention(const void *Q, had_dtype_t dt, const float *sigma_q,
+                                 const had_cache_t *cache, const int32_t *table, int max_pages,
+                                 const int32_t *lens, const int32_t *counts, int B, int Hq, int T,
+                                 int N, float tau, int window, int sinks, float *out,
+                                 int32_t *dev_status, cudaStream_t stream)
+{
+    CacheView c;
+    unsigned rows;
+    had_status_t s = check_cache(cache, &c);
+    if (s == HAD_OK && Hq < 1) s = HAD_ERR_INVALID_ARG;
+    if (s == HAD_OK) s = check_rows(B, Hq, T, &rows);
+    if (s == HAD_OK) s = check_table(table, B, max_pages, cache->page);
+    if (s != HAD_OK) return s;
+    if (Hq % c.heads != 0 || N < 1 || window < 0 || sinks < 0 || !finite_nonneg(tau))
+        return HAD_ERR_INVALID_ARG;
+    if (dt != HAD_BF16 && dt != HAD_F32) return HAD_ERR_INVALID_ARG;
+    if (!good(Q, 16) || !good(out, 16) || !good(sigma_q, 4) || !good(lens, 4) ||
+        !aligned(counts, 4) || !aligned(dev_status, 4))
+        return HAD_ERR_INVALID_ARG;
+    const had::CacheAttnArgs a{Q, sigma_q, c, table, lens, counts, max_pages, Hq, T, N, window,
+                               sinks, tau, out, dev_status};
+    if (dt == HAD_BF16) {
+        if (cache->d == 64)
+            had::cache_attn_row_kernel<__nv_bfloat16, 64><<<rows, had::kCacheAttnThreads, 0, stream>>>(a);
+        else
+            had::cache_attn_row_kernel<__nv_bfloat16, 128><<<rows, had::kCacheAttnThreads, 0, stream>>>(a);
+    } else {
+        if (cache->d == 64)
+            had::cache_attn_row_kernel<float, 64><<<rows, had::kCacheAttnThreads, 0, stream>>>(a);
+        else
+            had::cache_attn_row_kernel<float, 128><<<rows, had::kCacheAttnThreads, 0, stream>>>(a);
+    }
+    return launched();
+}
+
+had_status_t had_cache_fork(int32_t *table, int32_t *lens, int32_t *refs, int S, int max_pages,
+                            int pages, int page, const int32_t *src, const int32_t *dst, int n,
+                            int32_t *dev_status, cudaStream_t stream)
+{
+    Books k;
+    if (page == 1) return HAD_ERR_UNSUPPORTED;
+    const had_status_t s = check_books(table, lens, refs, S, max_pages, pages, page, &k);
+    if (s != HAD_OK) return s;
+    if (S > had::kMaxSeqs) return HAD_ERR_UNSUPPORTED;
+    if (n < 0 || n > S) return HAD_ERR_INVALID_ARG;
+    if (n == 0) return HAD_OK;
+    if (!good(src, 4) || !good(dst, 4) || !aligned(dev_status, 4)) return HAD_ERR_INVALID_ARG;
+    // whole 128-byte lines of a row per tile while shared memory holds them
+    int tile = 32;
+    while (tile > 1 && had::fork_smem_bytes(n, S, tile) > (size_t)kMaxSmem) --tile;
+    return launch_cluster(had::cache_fork_kernel, had::fork_smem_bytes(n, S, tile), stream, k, src,
+                          dst, n, tile, dev_status);
+}
+
+had_status_t had_cache_reserve(int32_t *table, const int32_t *lens, int32_t *refs, int S,
+                               int max_pages, int pages, int page, const int32_t *grow,
+                               int32_t *src, int32_t *dst, int32_t *dev_status,
+                               cudaStream_t stream)
+{
+    Books k;
+    if (page == 1) return HAD_ERR_UNSUPPORTED;
+    const had_status_t s = check_books(table, lens, refs, S, max_pages, pages, page, &k);
+    if (s != HAD_OK) return s;
+    if (S > had::kMaxSeqs) return HAD_ERR_UNSUPPORTED;
+    if (!good(grow, 4) || !good(src, 4) || !good(dst, 4) || !aligned(dev_status, 4))
+        return HAD_ERR_INVALID_ARG;
+    return launch_cluster(had::cache_reserve_kernel, had::reserve_smem_bytes(S), stream, k, grow,
+                          src, dst, dev_status);
+}
+
+had_status_t had_cache_free(int32_t *table, int32_t *lens, int32_t *refs, int S, int max_pages,
+                            int pages, const int32_t *seqs, int n, int32_t *dev_status,
+                            cudaStream_t stream)
+{
+    Books k;
+    const had_status_t s = check_books(table, lens, refs, S, max_pages, pages, 1, &k);
+    if (s != HAD_OK) return s;
+    if (n < 0) return HAD_ERR_INVALID_ARG;
+    if (n == 0) return HAD_OK;
+    if (!good(seqs, 4) || !aligned(dev_status, 4)) return HAD_ERR_INVALID_ARG;
+    had::cache_free_kernel<<<grid_for((long long)n * max_pages, 256), 256, 0, stream>>>(
+        k, seqs, n, dev_status);
+    return launched();
+}
+
+had_status_t had_cache_evict(int32_t *table, const int32_t *lens, int32_t *refs, int S,
+                             int max_pages, int pages, int page, int window, int sinks,
+                             int32_t *dev_status, cudaStream_t stream)
+{
+    Books k;
+    if (page == 1) return HAD_ERR_UNSUPPORTED;
+    const had_status_t s = check_books(table, lens, refs, S, max_pages, pages, page, &k);
+    if (s != HAD_OK) return s;
+    if (window < 1 || sinks < 0 || !aligned(dev_status, 4)) return HAD_ERR_INVALID_ARG;
+    had::cache_evict_kernel<<<grid_for((long long)S * max_pages, 256), 256, 0, stream>>>(
+        k, window, sinks, dev_status);
+    return launched();
+}
+
+had_status_t had_cache_compact(int32_t *table, int32_t *refs, int S, int max_pages, int pages,
+                               int32_t *src, int32_t *dst, int32_t *live, int32_t *dev_status,
+                               cudaStream_t stream)
+{
+    Books k;
+    const had_status_t s = check_books(table, refs, refs, S, max_pages, pages, 1, &k);
+    if (s != HAD_OK) return s;
+    if (!good(src, 4) || !good(dst, 4) || !good(live, 4) || !aligned(dev_status, 4))
+        return HAD_ERR_INVALID_ARG;
+    return launch_cluster(had::cache_compact_kernel, 0, stream, k, src, dst, live, dev_status);
+}
+
+had_status_t had_cache_copy_pages(const had_cache_t *cache, const int32_t *src,
+                                  const int32_t *dst, int n, int32_t *dev_status,
+                                  cudaStream_t stream)
+{
+    CacheView c;
+    const had_status_t s = check_cache(cache, &c);
+    if (s != HAD_OK) return s;
+    if (n < 0) return HAD_ERR_INVALID_ARG;
+    if (n == 0) return HAD_OK;
+    if (!good(src, 4) || !good(dst, 4) || !aligned(dev_status, 4)) return HAD_ERR_INVALID_ARG;
+    const long long rows = (long long)c.heads * cache->page, d = cache->d;
+    had::cache_copy_kernel<<<dim3(4, n < 65535 ? n : 65535), 256, 0, stream>>>(
+        c, rows * d / 128, rows * d / 32, rows / 4, src, dst, n, dev_status);
+    return launched();
+}
+
+}  // extern "C"

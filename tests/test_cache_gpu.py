@@ -1,0 +1,702 @@
+"""The decoder cache on the GPU against its 64-bit oracle.
+
+Bits, codes, scales and books have to be equal.  Attention is compared within
+    |err| <= (kept / 4 + 64) 2^-23 sum p (|c s| + |z|)
+per element: p carries at most 64 units of 2^-23 (the argument of exp up to 23
+in size and rounded once, exp to 2 units, a sum of at most 129 levels, one
+division), the products and the sum over at most a quarter of the kept tokens
+in one running fp32 value (four or more partial sums) the rest.  Where values
+are whole numbers and all weights equal, a wrong kept token shows as a whole
+count (test_kept_sets).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import cache as ocache
+
+pytestmark = pytest.mark.gpu
+I = torch.int32
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def cache():
+    from sparse_attention_sigma_b200 import cache as _cache
+    return _cache
+
+
+def ints(x):
+    return torch.tensor(x, dtype=I, device="cuda")
+
+
+def status():
+    return torch.zeros(1, dtype=I, device="cuda")
+
+
+def flags(st):
+    return int(st.item())
+
+
+INVALID, BAD_SIGMA, NO_PAGES = 1 << 1, 1 << 5, 1 << 7
+
+
+class Filled:
+    """A pool and books of sequences of the given lengths, filled by had_cache_append, and the
+    oracle's view of the same tokens."""
+
+    def __init__(self, cache, lens, H, d, page, dtype=BF16, seed=0, values=None, same_keys=False,
+                 spare=2):
+        g = torch.Generator().manual_seed(seed)
+        B, T = len(lens), max(max(lens), 1)
+        self.d, self.page, self.lens = d, page, lens
+        self.k = torch.randn(B, H, T, d, generator=g).to(dtype)
+        if same_keys:
+            self.k[:, :, 1:] = self.k[:, :, :1]
+        v = torch.randn(B, H, T, d, generator=g) if values is None else values(B, H, T, d)
+        self.v = v.to(dtype)
+        self.sigma = 0.5 + torch.rand(H, generator=g)
+        width = -(-T // page) + 1
+        need = [-(-n // page) for n in lens]
+        order = torch.randperm(sum(need) + spare, generator=g).to(I)
+        self.table = torch.full((B, width), -1, dtype=I)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        self.refs = torch.zeros(order.numel(), dtype=I)
+        self.refs[order[:at].long()] = 1
+        self.table, self.refs = self.table.cuda(), self.refs.cuda()
+        self.cache = cache.Cache.empty(order.numel(), H, page, d)
+        # what was there before shows wherever a kernel reads a place it should not
+        self.cache.kbits.fill_(-1)
+        self.cache.vcodes.fill_(255)
+        self.cache.vscale.fill_(float("nan"))
+        st = status()
+        cache.had_cache_append(self.k.cuda(), self.v.cuda(), self.sigma.cuda(), self.cache,
+                               self.table, ints([0] * B), counts=ints(lens), dev_status=st)
+        assert flags(st) == 0
+        self.sk = np.where(self.k.float().numpy() / self.sigma.numpy()[None, :, None, None] < 0,
+                           -1, 1)
+        self.codes, self.scale, self.zero = ocache.quantise(self.v.float().numpy())
+
+    def rows(self, q, sigma_q, lens, counts, N, tau, window, sinks):
+        """(out, bound) of the oracle for queries q [B, Hq, T, d]."""
+        B, Hq, T, d = q.shape
+        G = Hq // self.sk.shape[1]
+        sq = np.where(q.float().numpy() / sigma_q.numpy()[None, :, None, None] < 0, -1, 1)
+        out, bound = np.zeros(q.shape), np.zeros(q.shape)
+        for b in range(B):
+            for h in range(Hq):
+                for t in range(counts[b]):
+                    o, kept, size = ocache.attend(
+                        sq[b, h, t], self.sk[b, h // G], self.codes[b, h // G],
+                        self.scale[b, h // G], self.zero[b, h // G], N, np.float32(tau), window,
+                        sinks, lens[b] - counts[b] + t)
+                    out[b, h, t] = o
+                    bound[b, h, t] = (kept.size / 4 + 64) * 2.0 ** -23 * size
+        return out, bound
+
+
+def queries(B, Hq, T, d, dtype, seed=99):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(B, Hq, T, d, generator=g).to(dtype), 0.5 + torch.rand(Hq, generator=g)
+
+
+# ------------------------------------------------------------- append and read
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,page,T,start,counts", [
+    (1, 1, 16, 1, [0], None),
+    (3, 2, 16, 1, [15, 16, 33], None),
+    (3, 5, 32, 77, [5, 0, 31], [77, 0, 3]),
+    (2, 3, 256, 300, [255, 1], [300, 299]),
+    (2, 1, 64, 129, [0, 64], None),
+])
+def test_append_and_read_back(cache, dtype, d, B, H, page, T, start, counts):
+    g = torch.Generator().manual_seed(T + d)
+    k, v = (torch.randn(B, H, T, d, generator=g).to(dtype) for _ in range(2))
+    sigma = 0.5 + torch.rand(H, generator=g)
+    width = max(-(-(s + T) // page) for s in start)
+    table = torch.randperm(B * width, generator=g).to(I).reshape(B, width).cuda()
+    c = cache.Cache.empty(B * width, H, page, d)
+    c.vscale.fill_(7.0)
+    st = status()
+    cnt = None if counts is None else ints(counts)
+    cache.had_cache_append(k.cuda(), v.cuda(), sigma.cuda(), c, table, ints(start), counts=cnt,
+                           dev_status=st)
+    bits, values = cache.had_cache_read(c, table, ints(start), T, counts=cnt, dev_status=st)
+    assert flags(st) == 0
+    real = np.arange(T)[None] < np.array(counts or [T] * B)[:, None]
+    signs = np.where(k.float().numpy() / sigma.numpy()[None, :, None, None] < 0, -1, 1)
+    want = np.where(real[:, None, :, None], oracle.pack(signs).view(np.int32), 0)
+    assert np.array_equal(bits.cpu().numpy(), want)
+    code, s, z = ocache.quantise(v.float().numpy())
+    exact = code * s[..., None].astype(np.float64) + z[..., None]     # 4 + 8 bits and a bf16: exact
+    exact = np.where(real[:, None, :, None], exact, 0).astype(np.float32)
+    assert np.array_equal(values.cpu().numpy(), exact)
+    # nothing but the written places changed
+    touched = torch.zeros(B * width, page, dtype=torch.bool)
+    for b in range(B):
+        for t in range(T):
+            if real[b, t]:
+                touched[table[b, (start[b] + t) // page].item(), (start[b] + t) % page] = True
+    rest = ~touched[:, None, :].expand(-1, H, -1).cuda()
+    assert not c.kbits[rest].any() and not c.vcodes[rest].any()
+    assert (c.vscale[rest] == 7.0).all()
+
+
+def test_append_of_special_rows(cache):
+    """Constants, signed zeros, tiny and huge ranges, NaN and infinities; signs of -0, NaN and a
+    quotient that underflows."""
+    d = 64
+    v = torch.zeros(1, 1, 12, d)
+    v[0, 0, 1] = -0.0
+    v[0, 0, 2] = 0.1
+    v[0, 0, 3] = torch.linspace(-1e-40, 1e-40, d)
+    v[0, 0, 4] = torch.linspace(-1.6e38, 1.6e38, d)
+    v[0, 0, 5] = torch.linspace(-3.0e38, 3.0e38, d)             # the range passes fp32
+    v[0, 0, 6, 3] = float("nan")
+    v[0, 0, 7, 63] = float("inf")
+    v[0, 0, 8, 0] = -float("inf")
+    v[0, 0, 9] = torch.arange(d) * 2.0 ** -149
+    v[0, 0, 10] = 1.0 + torch.arange(d) * 2.0 ** -23
+    v[0, 0, 11] = -3.4e38                                        # no bf16 at or below it
+    k = torch.zeros(1, 1, 12, d)
+    k[0, 0, 0] = -0.0
+    k[0, 0, 1] = float("nan")
+    k[0, 0, 2] = -1e-45
+    k[0, 0, 3] = -float("inf")
+    c = cache.Cache.empty(1, 1, 16, d)
+    st = status()
+    cache.had_cache_append(k.cuda(), v.cuda(), torch.full((1,), 4.0, device="cuda"), c, ints([[0]]),
+                           ints([0]), dev_status=st)
+    code, s, z = ocache.quantise(v.numpy())
+    got = c.vcodes.cpu().numpy()[0, 0, :12]
+    assert np.array_equal(np.stack([got & 15, got >> 4], -1).reshape(12, d), code[0, 0])
+    got = c.vscale.float().cpu().numpy()[0, 0, :12]
+    assert np.array_equal(got[:, 0], s[0, 0], equal_nan=True)
+    assert np.array_equal(got[:, 1], z[0, 0], equal_nan=True)
+    assert np.isnan(s[0, 0, [5, 6, 7, 8, 11]]).all() and np.isfinite(s[0, 0, [0, 1, 2, 3, 4, 9, 10]]).all()
+    assert c.kbits[0, 0, :4].cpu().tolist() == [[0, 0], [0, 0], [0, 0], [-1, -1]]
+    assert flags(st) == 0
+
+
+def test_append_flags_what_it_cannot_place(cache):
+    k = torch.randn(4, 1, 2, 64, device="cuda")
+    c = cache.Cache.empty(2, 1, 16, 64)
+    table = ints([[0, -1], [1, 2], [1, 1], [0, 1]])
+    for start, counts, sigma, want in (
+            ([15, 0, 0, 0], [2, 0, 0, 0], 1.0, INVALID),         # behind the sequence's pages
+            ([0, 15, 0, 0], [0, 2, 0, 0], 1.0, INVALID),         # a page the pool lacks
+            ([0, 0, 31, 0], [0, 0, 2, 0], 1.0, INVALID),         # behind the table
+            ([0, 0, 0, -1], [0, 0, 0, 2], 1.0, INVALID),
+            ([0, 0, 0, 0], [3, 0, 0, 0], 1.0, INVALID),          # more than T
+            ([0, 0, 0, 0], [-1, 0, 0, 0], 1.0, INVALID),
+            ([0, 0, 0, 0], [0, 0, 0, 0], 1.0, 0),
+            ([0, 0, 0, 0], [0, 0, 0, 2], 0.0, BAD_SIGMA)):
+        st = status()
+        cache.had_cache_append(k, k, torch.full((1,), sigma, device="cuda"), c, table, ints(start),
+                               counts=ints(counts), dev_status=st)
+        assert flags(st) == want, (start, counts)
+        if sigma:
+            st = status()
+            cache.had_cache_read(c, table, ints(start), 2, counts=ints(counts), dev_status=st)
+            assert flags(st) == want
+
+
+# ------------------------------------------------------------------- attention
+
+ATTEND = [
+    # lens, Hq, Hkv, d, page, T, counts, N, window, sinks, dtype
+    ([1], 1, 1, 64, 16, 1, None, 1, 0, 0, BF16),
+    ([128], 2, 2, 64, 16, 1, None, 16, 0, 0, F32),
+    ([33, 0, 17], 4, 2, 128, 16, 1, None, 5, 0, 0, BF16),
+    ([300, 299, 1], 5, 1, 64, 32, 1, None, 1000, 0, 0, F32),
+    ([700], 6, 1, 128, 64, 1, None, 100, 0, 0, BF16),
+    ([1030, 515], 16, 2, 64, 128, 1, None, 64, 0, 0, BF16),
+    ([2500], 3, 3, 64, 256, 1, None, 2499, 0, 0, F32),
+    ([600, 40, 39], 8, 8, 128, 64, 1, None, 50, 40, 4, BF16),
+    ([100], 1, 1, 64, 16, 1, None, 3, 1, 0, F32),
+    ([100], 1, 1, 64, 16, 1, None, 3, 1, 33, F32),
+    ([70, 200], 2, 1, 64, 32, 1, None, 500, 64, 300, BF16),
+    ([50, 3, 0, 5], 4, 2, 64, 16, 5, [5, 4, 0, 5], 7, 0, 0, F32),
+    ([2, 1], 2, 2, 128, 16, 4, None, 3, 0, 0, BF16),             # more queries than tokens
+    ([65], 3, 1, 64, 64, 65, None, 9, 0, 0, BF16),
+    ([200, 130], 4, 2, 128, 32, 37, [37, 20], 300, 0, 0, F32),
+    ([333], 10, 2, 64, 32, 60, None, 20, 31, 5, BF16),
+    ([260], 7, 1, 64, 128, 33, None, 16, 100, 0, F32),
+    ([150], 11, 1, 128, 16, 3, None, 33, 20, 1, BF16),
+]
+
+
+@pytest.mark.parametrize("case", ATTEND, ids=lambda c: "-".join(map(str, c[:-1])).replace(" ", ""))
+def test_attention(cache, case):
+    lens, Hq, H, d, page, T, counts, N, window, sinks, dtype = case
+    f = Filled(cache, lens, H, d, page, dtype, seed=sum(lens) + d)
+    q, sigma_q = queries(len(lens), Hq, T, d, dtype)
+    tau = 1 / math.sqrt(d)
+    st = status()
+    out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, f.table, ints(lens), N, tau,
+                                    window=window, sinks=sinks,
+                                    counts=None if counts is None else ints(counts), dev_status=st)
+    assert flags(st) == 0
+    want, bound = f.rows(q, sigma_q, lens, counts or [T] * len(lens), N, tau, window, sinks)
+    err = np.abs(out.cpu().numpy() - want)
+    assert (err <= bound).all(), (err - bound).max()
+
+
+def _marks(B, H, T, d):
+    """Values of which element e is 15 where token j has j mod d = e, else 0: codes 15 and 0,
+    scale 1, zero point 0."""
+    v = torch.zeros(B, H, T, d)
+    j = torch.arange(T)
+    v[:, :, j, j % d] = 15.0
+    return v
+
+
+@pytest.mark.parametrize("lens,G,T,N,window,sinks,same", [
+    ([100], 1, 1, 50, 0, 0, True),               # one level: ties only, the lowest indices win
+    ([1000], 4, 1, 333, 0, 0, True),
+    ([5000], 3, 1, 1234, 0, 0, True),
+    ([5000], 8, 1, 777, 0, 0, False),
+    ([900, 31], 2, 9, 200, 0, 0, False),
+    ([900, 310], 4, 50, 100, 333, 7, True),
+    ([20000], 1, 1, 9000, 0, 0, False),
+    ([9000], 5, 2, 4000, 6000, 100, False),
+])
+@pytest.mark.parametrize("d", [64, 128])
+def test_kept_sets(cache, d, lens, G, T, N, window, sinks, same):
+    """With tau 0 every kept token weighs 1 / n, so n out[e] counts the kept tokens of each
+    residue: exact sets, ties included."""
+    f = Filled(cache, lens, 1, d, 64, F32, seed=G + N, values=_marks, same_keys=same)
+    q, sigma_q = queries(len(lens), G, T, d, F32)
+    st = status()
+    out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, f.table, ints(lens), N, 0.0,
+                                    window=window, sinks=sinks, dev_status=st).cpu().numpy()
+    assert flags(st) == 0
+    sq = np.where(q.numpy() / sigma_q.numpy()[None, :, None, None] < 0, -1, 1)
+    for b, n in enumerate(lens):
+        for h in range(G):
+            for t in range(T):
+                _, kept, _ = ocache.attend(sq[b, h, t], f.sk[b, 0], f.codes[b, 0], f.scale[b, 0],
+                                           f.zero[b, 0], N, 0.0, window, sinks, n - T + t)
+                count = np.bincount(kept % d, minlength=d)
+                got = out[b, h, t] * kept.size / 15
+                assert np.array_equal(np.rint(got), count)
+                assert np.abs(got - count).max() < 0.01
+
+
+def test_values_of_any_size_keep_their_weight(cache):
+    """Tokens whose scales differ by 60 orders of magnitude: each output element is as exact as
+    its own sum allows."""
+    def values(B, H, T, d):
+        g = torch.Generator().manual_seed(4)
+        return torch.randn(B, H, T, d, generator=g) * 10.0 ** torch.randint(-30, 31, (B, H, T, 1),
+                                                                             generator=g)
+    f = Filled(cache, [400], 2, 64, 32, F32, values=values)
+    q, sigma_q = queries(1, 4, 1, 64, F32)
+    out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, f.table, ints([400]), 60, 0.5)
+    want, bound = f.rows(q, sigma_q, [400], [1], 60, 0.5, 0, 0)
+    assert (np.abs(out.cpu().numpy() - want) <= bound).all()
+
+
+@pytest.mark.parametrize("tau", [0.0, 3.0, 1e30])
+def test_temperatures(cache, tau):
+    f = Filled(cache, [300], 1, 64, 16, F32)
+    q, sigma_q = queries(1, 2, 1, 64, F32)
+    out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, f.table, ints([300]), 40, tau)
+    want, bound = f.rows(q, sigma_q, [300], [1], 40, tau, 0, 0)
+    # exp's argument reaches 128 tau: its rounding is 128 tau 2^-24 relative where it matters
+    assert (np.abs(out.cpu().numpy() - want) <= bound * (1 + min(tau, 10.0))).all()
+
+
+def test_rows_that_keep_an_unholdable_value_are_nan_and_no_others(cache):
+    def values(B, H, T, d):
+        v = torch.ones(B, H, T, d)
+        v[0, 0, 10, 5] = float("nan")
+        return v
+    f = Filled(cache, [64], 2, 64, 16, F32, values=values)
+    q, sigma_q = queries(1, 4, 64, 64, F32)
+    out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, f.table, ints([64]), 8, 0.1)
+    want, _ = f.rows(q, sigma_q, [64], [64], 8, 0.1, 0, 0)
+    got = out.cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.isnan(got).any() and not np.isnan(got[:, 2:]).any()
+    assert np.abs(got[~np.isnan(got)][np.nonzero(got[~np.isnan(got)])] - 1).max() < 1e-5
+
+
+def test_attention_flags_bad_books(cache):
+    f = Filled(cache, [100, 100], 1, 64, 16, F32)
+    q, sigma_q = queries(2, 1, 2, 64, F32)
+    args = q.cuda(), sigma_q.cuda(), f.cache
+
+    def run(table, lens, counts=None, sigma=None):
+        st = status()
+        out = cache.had_cache_attention(args[0], args[1] if sigma is None else sigma, args[2],
+                                        table, ints(lens), 5, 0.1, dev_status=st,
+                                        counts=None if counts is None else ints(counts))
+        return flags(st), out
+
+    clean = run(f.table, [100, 100])
+    assert clean[0] == 0
+    for page in (-1, -7, f.cache.pages, 2 ** 31 - 1):
+        t = f.table.clone()
+        t[0, 3] = page
+        flag, out = run(t, [100, 100])
+        assert flag == INVALID and torch.equal(out[1], clean[1][1])
+    for lens, counts in (([-1, 100], None), ([f.table.shape[1] * 16 + 1, 100], None),
+                         ([100, 100], [3, 2]), ([100, 100], [-1, 2])):
+        flag, out = run(f.table, lens, counts)
+        assert flag == INVALID and not out[0].any() and torch.equal(out[1], clean[1][1])
+    flag, _ = run(f.table, [100, 100], sigma=torch.full((1,), -1.0, device="cuda"))
+    assert flag == BAD_SIGMA
+
+
+def test_padded_rows_are_zero_and_evicted_pages_are_not_read(cache):
+    """Under a window the pages before it may be gone; rows behind a count get zeros."""
+    W, S, n = 40, 5, 400
+    f = Filled(cache, [n], 2, 64, 16, BF16)
+    q, sigma_q = queries(1, 4, 3, 64, BF16)
+    run = lambda table, st: cache.had_cache_attention(                    # noqa: E731
+        q[:, :, :2].contiguous().cuda(), sigma_q.cuda(), f.cache, table, ints([n]), 16, 0.1,
+        window=W, sinks=S, counts=ints([1]), dev_status=st)
+    st = status()
+    before = run(f.table, st)
+    table = f.table.clone()
+    cache.had_cache_evict(table, ints([n]), f.refs, 16, W, S)
+    assert (table == -1).sum() > (f.table == -1).sum() + 10
+    after = run(table, st)
+    assert flags(st) == 0 and torch.equal(before, after)
+    assert not after[:, :, 1].any() and after[:, :, 0].any()
+
+
+# --------------------------------------------------------------- pages' books
+
+def _same_books(table, lens, refs, b):
+    t, n, r = b.arrays()
+    assert np.array_equal(table.cpu().numpy(), t)
+    assert np.array_equal(lens.cpu().numpy(), n)
+    assert np.array_equal(refs.cpu().numpy(), r)
+
+
+@pytest.mark.parametrize("S,width,P,page,seed", [
+    (1, 3, 5, 16, 0), (5, 9, 40, 16, 1), (7, 5, 30, 256, 2), (64, 40, 1500, 64, 3),
+    (33, 70, 900, 32, 4), (3, 1, 3, 128, 5)])
+def test_books_through_a_run(cache, S, width, P, page, seed):
+    """Forks, growth, eviction, departures and compactions in turn, as a beam server has them."""
+    g = np.random.default_rng(seed)
+    table, lens, refs = cache.empty_books(S, width, P)
+    b = ocache.Books(table, lens, refs, page)
+    st = status()
+    full = 0
+    for step in range(30):
+        grow = g.integers(0, max(2, width * page // 6), S) * (g.random(S) < 0.7)
+        grow = np.minimum(grow, width * page - np.array(b.lens))
+        src, dst = cache.had_cache_reserve(table, lens, refs, page, ints(grow.tolist()),
+                                           dev_status=st)
+        want = b.reserve(grow.tolist())
+        if want is None:
+            assert flags(st) == NO_PAGES
+            st.zero_()
+            full += 1
+            want = [-1] * S, [-1] * S
+        else:
+            lens += ints(grow.tolist())
+            b.lens = [n + int(x) for n, x in zip(b.lens, grow)]
+        assert src.tolist() == want[0] and dst.tolist() == want[1]
+        _same_books(table, lens, refs, b)
+        n = int(g.integers(0, S + 1))
+        to = g.permutation(S)[:n]
+        frm = g.integers(0, S, n)
+        cache.had_cache_fork(table, lens, refs, page, ints(frm.tolist()), ints(to.tolist()),
+                             dev_status=st)
+        b.fork(frm.tolist(), to.tolist())
+        _same_books(table, lens, refs, b)
+        if step % 3 == 1:
+            W, sinks = int(g.integers(1, width * page)), int(g.integers(0, 2 * page))
+            cache.had_cache_evict(table, lens, refs, page, W, sinks, dev_status=st)
+            b.evict(W, sinks)
+        if step % 4 == 2 or full:
+            full = 0
+            gone = g.integers(0, S, S // 2 + 1)                   # some listed twice
+            cache.had_cache_free(table, lens, refs, ints(gone.tolist()), dev_status=st)
+            b.free(gone.tolist())
+            _same_books(table, lens, refs, b)
+            src, dst, live = cache.had_cache_compact(table, refs, dev_status=st)
+            want = b.compact()
+            assert (src.tolist(), dst.tolist(), live.item()) == want
+        _same_books(table, lens, refs, b)
+        assert flags(st) == 0
+        counted = np.bincount(table[table >= 0].cpu().numpy(), minlength=P)
+        assert np.array_equal(counted, refs.cpu().numpy())
+
+
+def test_books_of_a_large_pool(cache):
+    """More pages and sequences than one pass of a CTA over them covers."""
+    S, width, P, page = 3000, 20, 70001, 16
+    g = np.random.default_rng(11)
+    table, lens, refs = cache.empty_books(S, width, P)
+    b = ocache.Books(table, lens, refs, page)
+    grow = g.integers(0, width * page - 40, S)
+    cache.had_cache_reserve(table, lens, refs, page, ints(grow.tolist()))
+    b.reserve(grow.tolist())
+    lens += ints(grow.tolist())
+    b.lens = grow.tolist()
+    to = g.permutation(S)[:S // 2]
+    frm = g.integers(0, S, to.size)
+    cache.had_cache_fork(table, lens, refs, page, ints(frm.tolist()), ints(to.tolist()))
+    b.fork(frm.tolist(), to.tolist())
+    _same_books(table, lens, refs, b)
+    src, dst = cache.had_cache_reserve(table, lens, refs, page, ints([1] * S))
+    assert (src.tolist(), dst.tolist()) == b.reserve([1] * S)
+    _same_books(table, lens, refs, b)
+    gone = list(range(0, S, 3))
+    cache.had_cache_free(table, lens, refs, ints(gone))
+    b.free(gone)
+    src, dst, live = cache.had_cache_compact(table, refs)
+    assert (src.tolist(), dst.tolist(), live.item()) == b.compact()
+    _same_books(table, lens, refs, b)
+
+
+def test_books_refuse_and_stay_as_they_were(cache):
+    page = 16
+    table, lens, refs = ints([[0, 1, -1], [2, -1, -1]]), ints([20, 10]), ints([1, 1, 1, 0])
+    start = [x.clone() for x in (table, lens, refs)]
+
+    def unchanged(want, st):
+        assert flags(st) == want
+        assert all(torch.equal(a, x) for a, x in zip(start, (table, lens, refs)))
+        st.zero_()
+
+    st = status()
+    for grow, want in (([40, 0], INVALID), ([-1, 1], INVALID), ([13, 20], NO_PAGES)):
+        src, dst = cache.had_cache_reserve(table, lens, refs, page, ints(grow), dev_status=st)
+        assert src.tolist() == dst.tolist() == [-1, -1]
+        unchanged(want, st)
+    for src, dst in (([0, 0], [1, 1]), ([2], [0]), ([0], [-1]), ([-1], [0]), ([0], [2])):
+        cache.had_cache_fork(table, lens, refs, page, ints(src), ints(dst), dev_status=st)
+        unchanged(INVALID, st)
+    bad = lens.clone()
+    bad[0] = 49
+    cache.had_cache_fork(table, bad, refs, page, ints([0]), ints([1]), dev_status=st)
+    unchanged(INVALID, st)
+    src, dst = cache.had_cache_reserve(table, bad, refs, page, ints([0, 0]), dev_status=st)
+    unchanged(INVALID, st)
+    # the last page is not there
+    hole = ints([[0, -1, -1], [2, -1, -1]])
+    cache.had_cache_reserve(hole, lens, refs, page, ints([1, 0]), dev_status=st)
+    assert hole.tolist() == [[0, -1, -1], [2, -1, -1]]
+    unchanged(INVALID, st)
+    cache.had_cache_free(table, lens, refs, ints([-1, 2]), dev_status=st)
+    unchanged(INVALID, st)
+    # names that are no pages are dropped by free and stay in compact
+    wild = ints([[9, 1, -1], [2, -1, -1]])
+    cache.had_cache_compact(wild, refs.clone(), dev_status=st)
+    assert flags(st) == INVALID and wild.tolist() == [[9, 1, -1], [2, -1, -1]]
+    st.zero_()
+    r = refs.clone()
+    cache.had_cache_free(wild, lens.clone(), r, ints([0]), dev_status=st)
+    assert flags(st) == INVALID and r.tolist() == [1, 0, 1, 0] and wild[0].tolist() == [-1] * 3
+
+
+@pytest.mark.parametrize("d,page,H", [(64, 16, 1), (128, 64, 3), (64, 256, 2)])
+def test_copy_pages(cache, d, page, H):
+    P = 40
+    c = cache.Cache.empty(P, H, page, d)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for a in (c.kbits, c.vcodes, c.vscale.view(torch.int16)):
+        a.copy_(torch.randint(-2 ** 15, 2 ** 15, a.shape, generator=g, device="cuda"))
+    raw = [a.view(torch.uint8).reshape(P, -1).clone() for a in (c.kbits, c.vcodes, c.vscale)]
+    src = [0, 3, 3, -1, 7, P, 9, -1] + [11] * 9
+    dst = [20, 21, 22, 23, -1, 24, P, -1] + list(range(30, 39))
+    st = status()
+    cache.had_cache_copy_pages(c, ints(src), ints(dst), dev_status=st)
+    assert flags(st) == INVALID
+    want = [r.clone() for r in raw]
+    for s, t in zip(src, dst):
+        if 0 <= s < P and 0 <= t < P:
+            for r, w in zip(raw, want):
+                w[t] = r[s]
+    for a, w in zip((c.kbits, c.vcodes, c.vscale), want):
+        assert torch.equal(a.view(torch.uint8).reshape(P, -1), w)
+
+
+# ------------------------------------------------------------- used together
+
+def _decode(cache, steps, stream=None):
+    """Two sequences of a prompt, forked into four that go on, d 64, window and sinks."""
+    B, H, G, d, page, N, W, S = 4, 2, 3, 64, 16, 12, 48, 4
+    g = torch.Generator().manual_seed(2)
+    table, lens, refs = cache.empty_books(B, 10, 60)
+    c = cache.Cache.empty(60, H, page, d)
+    sk, sq = (0.5 + torch.rand(H, generator=g)).cuda(), (0.5 + torch.rand(G * H, generator=g)).cuda()
+    hist_k = [torch.zeros(H, 0, d) for _ in range(B)]
+    hist_v = [torch.zeros(H, 0, d) for _ in range(B)]
+    st = status()
+
+    def step(T, counts, Nq):
+        k, v = (torch.randn(B, H, T, d, generator=g) for _ in range(2))
+        q = torch.randn(B, G * H, T, d, generator=g)
+        grow = ints(counts)
+        src, dst = cache.had_cache_reserve(table, lens, refs, page, grow, dev_status=st,
+                                           stream=stream)
+        cache.had_cache_copy_pages(c, src, dst, dev_status=st, stream=stream)
+        cache.had_cache_append(k.cuda(), v.cuda(), sk, c, table, lens, counts=grow, dev_status=st,
+                               stream=stream)
+        lens.add_(grow)
+        out = cache.had_cache_attention(q.cuda(), sq, c, table, lens, Nq, 0.125, window=W, sinks=S,
+                                        counts=grow, dev_status=st, stream=stream)
+        cache.had_cache_evict(table, lens, refs, page, W, S, dev_status=st, stream=stream)
+        worst = 0.0
+        for b, n in enumerate(counts):
+            hist_k[b] = torch.cat([hist_k[b], k[b, :, :n]], 1)
+            hist_v[b] = torch.cat([hist_v[b], v[b, :, :n]], 1)
+            code, s, z = ocache.quantise(hist_v[b].numpy())
+            for h in range(G * H):
+                signs = np.where(hist_k[b][h // G].numpy() / sk[h // G].item() < 0, -1, 1)
+                for t in range(n):
+                    row = np.where(q[b, h, t].numpy() / sq[h].item() < 0, -1, 1)
+                    o, kept, size = ocache.attend(row, signs, code[h // G], s[h // G], z[h // G],
+                                                  Nq, np.float32(0.125), W, S,
+                                                  hist_k[b].shape[1] - n + t)
+                    err = np.abs(out[b, h, t].cpu().numpy() - o)
+                    worst = max(worst, (err / ((kept.size / 4 + 64) * 2.0 ** -23 * size)).max())
+        assert worst <= 1 and flags(st) == 0
+
+    step(70, [70, 33, 0, 0], 20)
+    src, dst = [0, 1], [2, 3]
+    cache.had_cache_fork(table, lens, refs, page, ints(src), ints(dst), dev_status=st, stream=stream)
+    for s, t in zip(src, dst):
+        hist_k[t], hist_v[t] = hist_k[s], hist_v[s]
+    for i in range(steps):
+        step(1, [1] * B, N)
+        if i % 3 == 1:
+            order = [1, 0, 0, 3] if i % 2 else [2, 1, 2, 0]
+            cache.had_cache_fork(table, lens, refs, page, ints(order), ints(range(B)), dev_status=st,
+                                 stream=stream)
+            hist_k[:], hist_v[:] = [hist_k[o] for o in order], [hist_v[o] for o in order]
+        if i == 5:
+            cache.had_cache_free(table, lens, refs, ints([3]), dev_status=st, stream=stream)
+            hist_k[3] = hist_v[3] = torch.zeros(H, 0, d)
+            src, dst, live = cache.had_cache_compact(table, refs, dev_status=st, stream=stream)
+            cache.had_cache_copy_pages(c, src, dst, dev_status=st, stream=stream)
+            assert live.item() == torch.unique(table[table >= 0]).numel()
+    step(4, [4, 3, 1, 0], N)
+    counted = np.bincount(table[table >= 0].cpu().numpy(), minlength=60)
+    assert np.array_equal(counted, refs.cpu().numpy())
+
+
+def test_decoding_with_forks_growth_eviction_and_compaction(cache):
+    _decode(cache, 12)
+
+
+def test_calls_go_to_the_given_stream(cache):
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        _decode(cache, 4, stream=s)
+
+
+def test_a_chunked_prompt_is_the_causal_forward(cache):
+    """A prompt in three chunks through the cache against had_attention_causal_fwd on the values
+    that the cache holds, within that call's tolerance."""
+    from sparse_attention_sigma_b200 import had
+    B, H, n, d, N, tau = 2, 3, 300, 64, 40, 0.125
+    f = Filled(cache, [n] * B, H, d, 64, F32, seed=8)
+    q, sigma_q = queries(B, H, n, d, F32)
+    _, values = cache.had_cache_read(f.cache, f.table, ints([0] * B), n)
+    want = had.had_attention_causal_fwd(q.cuda(), f.k.cuda(), values, sigma_q.cuda(),
+                                        f.sigma.cuda(), N, tau)
+    at = 0
+    for chunk in (100, 1, 199):
+        out = cache.had_cache_attention(q[:, :, at:at + chunk].contiguous().cuda(), sigma_q.cuda(),
+                                        f.cache, f.table, ints([at + chunk] * B), N, tau)
+        assert (out - want[:, :, at:at + chunk]).abs().max() <= 2e-3
+        at += chunk
+
+
+def test_a_captured_step_replays_on_new_contents(cache):
+    """reserve, copy, append and attend in one graph: replays go on where the books stand, two
+    graphs of the same shapes side by side."""
+    H, G, d, page, N = 2, 2, 64, 16, 9
+    runs = []
+    for seed in (0, 1):
+        f = Filled(cache, [30, 47], H, d, page, F32, seed=seed, spare=20)
+        lens, grow = ints(f.lens), ints([1, 1])
+        table = torch.full((2, 8), -1, dtype=I, device="cuda")
+        table[:, :f.table.shape[1]] = f.table
+        k, v = (torch.zeros(2, H, 1, d, device="cuda") for _ in range(2))
+        q, sq = torch.zeros(2, G * H, 1, d, device="cuda"), torch.ones(G * H, device="cuda")
+        sk = f.sigma.cuda()
+        st = status()
+
+        def step():
+            src, dst = cache.had_cache_reserve(table, lens, f.refs, page, grow, dev_status=st)
+            cache.had_cache_copy_pages(f.cache, src, dst, dev_status=st)
+            cache.had_cache_append(k, v, sk, f.cache, table, lens, dev_status=st)
+            lens.add_(grow)
+            return cache.had_cache_attention(q, sq, f.cache, table, lens, N, 0.125, dev_status=st)
+
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        runs.append((f, graph, k, v, q, out, st, lens, [f.k, f.v], (table, grow, sq, sk)))
+    g = torch.Generator().manual_seed(5)
+    for _ in range(20):
+        for f, graph, k, v, q, out, st, lens, hist, _ in runs:
+            for x in (k, v, q):
+                x.copy_(torch.randn(x.shape, generator=g))
+            graph.replay()
+            if hist[0].shape[2] < lens.max().item():
+                hist[:] = [torch.cat([h, torch.zeros(2, H, 1, d)], 2) for h in hist]
+            for b, n in enumerate(lens.tolist()):
+                hist[0][b, :, n - 1], hist[1][b, :, n - 1] = k[b, :, 0].cpu(), v[b, :, 0].cpu()
+            assert flags(st) == 0
+            f.sk = np.where(hist[0].numpy() / f.sigma.numpy()[None, :, None, None] < 0, -1, 1)
+            f.codes, f.scale, f.zero = ocache.quantise(hist[1].numpy())
+            want, bound = f.rows(q.cpu(), torch.ones(G * H), lens.tolist(), [1, 1], N, 0.125, 0, 0)
+            assert (np.abs(out.cpu().numpy() - want) <= bound).all()
+
+
+def test_results_do_not_depend_on_the_run(cache):
+    f = Filled(cache, [3000, 2000], 2, 128, 64, BF16)
+    q, sigma_q = queries(2, 8, 2, 128, BF16)
+    run = lambda: cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, f.table,  # noqa: E731
+                                            ints([3000, 2000]), 500, 0.1)
+    first = run()
+    assert all(torch.equal(first, run()) for _ in range(5))
+
+
+def test_refusals_of_the_binding(cache):
+    f = Filled(cache, [20], 2, 64, 16, F32)
+    q, s = torch.zeros(1, 4, 1, 64, device="cuda"), torch.ones(4, device="cuda")
+    ok = dict(q=q, sigma_q=s, cache=f.cache, table=f.table, lens=ints([20]), N=4, tau=0.1)
+    cache.had_cache_attention(**ok)
+    for change, error in (
+            (dict(q=q.half()), TypeError), (dict(q=q.transpose(1, 2)), ValueError),
+            (dict(q=q[..., :32].contiguous()), ValueError), (dict(q=q[0]), ValueError),
+            (dict(sigma_q=s[:2]), ValueError), (dict(sigma_q=s.double()), TypeError),
+            (dict(table=f.table.long()), TypeError), (dict(table=f.table[0]), ValueError),
+            (dict(table=f.table.repeat(2, 1)), ValueError), (dict(lens=ints([20, 20])), ValueError),
+            (dict(lens=torch.tensor([20], device="cuda")), TypeError),
+            (dict(counts=ints([1, 1])), ValueError), (dict(N=0), cache.HadError),
+            (dict(tau=-1.0), cache.HadError), (dict(window=-1), cache.HadError),
+            (dict(window=2 ** 31), ValueError), (dict(sinks=-1), cache.HadError),
+            (dict(out=torch.zeros(1, 4, 1, 64)), ValueError), (dict(cache=f.cache.kbits), TypeError),
+            (dict(q=q[:, :3].contiguous(), sigma_q=s[:3]), cache.HadError),
+            (dict(dev_status=torch.zeros(2, dtype=I, device="cuda")), ValueError)):
+        with pytest.raises(error):
+            cache.had_cache_attention(**dict(ok, **change))
+    k = torch.zeros(1, 2, 1, 64, device="cuda")
+    with pytest.raises(ValueError):
+        cache.had_cache_append(k[:, :1].contiguous(), k, s[:2], f.cache, f.table, ints([0]))
+    with pytest.raises(TypeError):
+        cache.had_cache_append(k, k.bfloat16(), s[:2], f.cache, f.table, ints([0]))
+    with pytest.raises(ValueError):
+        cache.Cache(f.cache.kbits, f.cache.vcodes[:, :1].contiguous(), f.cache.vscale)
+    with pytest.raises(cache.HadError):
+        cache.had_cache_read(f.cache, f.table, ints([0]), 0)
