@@ -75,6 +75,10 @@ def _dev(t, name, dtype, ndim, device=None):
     """``t`` as a contiguous CUDA tensor of this type and number of dimensions."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    # a decode step makes these checks dozens of times: one test when all is well
+    if t.is_cuda and t.is_contiguous() and t.dim() == ndim and \
+            (dtype is None or t.dtype is dtype) and (device is None or t.device == device):
+        return t
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the HAD library has no CPU path)")
     if not t.is_contiguous():
@@ -83,9 +87,7 @@ def _dev(t, name, dtype, ndim, device=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-    return t
+    raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
 
 
 def _ints(t, name, n, device):
@@ -102,9 +104,14 @@ def _opt(t, name, n, device):
 
 def _shaped(t, name, dtype, shape, device):
     _dev(t, name, dtype, len(shape), device)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     return t
+
+
+# Handles without the Python objects around them (2 us of a call each).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 class _on:
@@ -115,14 +122,14 @@ class _on:
 
     def __init__(self, device, stream):
         self.stack = None
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        if stream is not None or torch.cuda.current_device() != device.index:
+        if stream is not None or _current_device() != device.index:
+            if stream is not None and stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
             self.stack = contextlib.ExitStack()
             self.stack.enter_context(torch.cuda.device(device))
             if stream is not None:
                 self.stack.enter_context(torch.cuda.stream(stream))
-        self.handle = torch.cuda.current_stream(device).cuda_stream
+        self.handle = _raw_stream(device.index)
 
     def __enter__(self):
         return self.handle
@@ -155,8 +162,7 @@ class Cache:
         _dev(vcodes, "vcodes", torch.uint8, 4, kbits.device)
         _dev(vscale, "vscale", torch.bfloat16, 4, kbits.device)
         pages, heads, page, words = kbits.shape
-        if vcodes.shape != (pages, heads, page, 16 * words) or \
-                vscale.shape != (pages, heads, page, 2):
+        if vcodes.shape != (pages, heads, page, 16 * words) or vscale.shape != (pages, heads, page, 2):
             raise ValueError("kbits, vcodes and vscale must be [pages, heads, page, d/32], "
                              f"[.., d/2] and [.., 2], got {tuple(kbits.shape)}, "
                              f"{tuple(vcodes.shape)} and {tuple(vscale.shape)}")

@@ -12,6 +12,7 @@
 namespace {
 
 using had::Books;
+using had::CacheTokens;
 using had::CacheView;
 
 constexpr int kMaxSmem = 227 * 1024;   // dynamic shared memory a CTA may have
@@ -43,8 +44,8 @@ had_status_t check_cache(const had_cache_t *c, CacheView *view)
     if (!c || c->pages < 1 || c->heads < 1 || c->d < 1) return HAD_ERR_INVALID_ARG;
     if (c->d != 64 && c->d != 128) return HAD_ERR_UNSUPPORTED;
     if (!good_page(c->page)) return HAD_ERR_UNSUPPORTED;
-    // rows and bytes of the pool stay far inside 64 bits
-    if ((long long)c->pages * c->heads > (1LL << 40) / c->page) return HAD_ERR_UNSUPPORTED;
+    // a (page, head, slot) row has a 32-bit index, and 2^32 - 1 stands for none
+    if ((long long)c->pages * c->heads >= (1LL << 32) / c->page) return HAD_ERR_UNSUPPORTED;
     if (!good(c->kbits, 16) || !good(c->vcodes, 16) || !good(c->vscale, 16))
         return HAD_ERR_INVALID_ARG;
     view->kbits = c->kbits;
@@ -73,27 +74,77 @@ had_status_t check_books(int32_t *table, const int32_t *lens, int32_t *refs, int
     return s;
 }
 
-// A launch of one cluster of the page operators.
+// A launch in clusters of `ctas` CTAs.
 template <typename... Params, typename... Args>
-had_status_t launch_cluster(void (*kernel)(Params...), size_t smem, cudaStream_t st, Args... args)
+had_status_t launch_clusters(void (*kernel)(Params...), unsigned grid, unsigned ctas,
+                             unsigned threads, size_t smem, cudaStream_t st, Args... args)
 {
-    // Set on every call: the attribute belongs to the current device.
-    if (smem > 48 * 1024 &&
+    // 48 KB, the kernel's own variables included, need no attribute.  Set on
+    // every call: it belongs to the current device.
+    if (smem > 24 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
             cudaSuccess)
         return HAD_ERR_CUDA;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim = {had::kBookCtas, 1, 1};
+    attr.val.clusterDim = {ctas, 1, 1};
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(had::kBookCtas);
-    cfg.blockDim = dim3(had::kBookThreads);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
     return e == cudaSuccess ? launched() : HAD_ERR_CUDA;
+}
+
+// A launch of one cluster of the page operators.
+template <typename... Params, typename... Args>
+had_status_t launch_cluster(void (*kernel)(Params...), size_t smem, cudaStream_t st, Args... args)
+{
+    return launch_clusters(kernel, had::kBookCtas, had::kBookCtas, had::kBookThreads, smem, st,
+                           args...);
+}
+
+template <typename T, int D, int NA>
+had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, had::CacheAttnPlan plan,
+                                   cudaStream_t st)
+{
+    const long long rows = (long long)(a.Hq / a.c.heads) * a.T;      // per key-value head
+    plan.tiles = (int)((rows + had::cache_attn_rows(NA) - 1) / had::cache_attn_rows(NA));
+    plan.R = (int)((rows + plan.tiles - 1) / plan.tiles);
+    plan.tiles = (int)((rows + plan.R - 1) / plan.R);
+    // the most keys a tile may see: the device alone knows the lengths
+    long long keys = (long long)a.max_pages << a.c.page_log;
+    if (a.window > 0) {
+        const long long seen = (long long)a.window + a.sinks + plan.R;
+        keys = seen < keys ? seen : keys;
+    }
+    // 48 KB of rows and distances at once, so that two CTAs share an SM
+    const long long most = 48 * 1024 / had::cache_attn_key_bytes(plan.R) / 256 * 256;
+    // CTAs until two per SM are busy, each with 256 keys or more, and until a
+    // CTA holds its slice whole (a longer one is gone through twice)
+    const long long tiles = (long long)B * a.c.heads * plan.tiles;
+    plan.ctas = 1;
+    while (plan.ctas < 8 && (keys + 32 * plan.ctas > most * plan.ctas ||
+                             (tiles * plan.ctas * 2 <= 2 * 148 && keys > 256LL * plan.ctas)))
+        plan.ctas *= 2;
+    const long long per = ((keys + plan.ctas - 1) / plan.ctas + 32 + 255) / 256 * 256;
+    plan.cap = (int)(per < most ? per : most);
+    if (tiles * plan.ctas > INT_MAX) return HAD_ERR_UNSUPPORTED;
+    return launch_clusters(had::cache_attn_kernel<T, D, NA>, (unsigned)(tiles * plan.ctas),
+                           (unsigned)plan.ctas, had::kCacheAttnThreads,
+                           had::cache_attn_smem_bytes<D, NA>(plan), st, a, plan);
+}
+
+template <typename T, int D>
+had_status_t launch_attention(const had::CacheAttnArgs &a, int B, cudaStream_t st)
+{
+    const had::CacheAttnPlan plan{};
+    return (long long)(a.Hq / a.c.heads) * a.T <= had::cache_attn_rows(1)
+               ? launch_attention_tile<T, D, 1>(a, B, plan, st)
+               : launch_attention_tile<T, D, 2>(a, B, plan, st);
 }
 
 unsigned grid_for(long long items, int per_block)
@@ -104,27 +155,31 @@ unsigned grid_for(long long items, int per_block)
 
 template <typename T>
 void launch_append(const void *K, const void *V, const float *sigma, const CacheView &c, int d,
-                   const int32_t *table, int max_pages, const int32_t *start,
-                   const int32_t *counts, int T_, unsigned rows, int32_t *status, cudaStream_t st)
+                   const CacheTokens &k, unsigned grid, int32_t *status, cudaStream_t st)
 {
-    const auto *k = static_cast<const T *>(K), *v = static_cast<const T *>(V);
-    const unsigned grid = (rows + 15) / 16;
+    const auto *key = static_cast<const T *>(K), *value = static_cast<const T *>(V);
     if (d == 64)
-        had::cache_append_kernel<T, 64><<<grid, 256, 0, st>>>(k, v, sigma, c, table, max_pages,
-                                                              start, counts, T_, rows, status);
+        had::cache_append_kernel<T, 64><<<grid, 256, 0, st>>>(key, value, sigma, c, k, status);
     else
-        had::cache_append_kernel<T, 128><<<grid, 256, 0, st>>>(k, v, sigma, c, table, max_pages,
-                                                               start, counts, T_, rows, status);
+        had::cache_append_kernel<T, 128><<<grid, 256, 0, st>>>(key, value, sigma, c, k, status);
 }
 
-// Rows (b, head, token) of an append or a read: one 16-lane group each.
-had_status_t check_rows(int B, int heads, int T, unsigned *rows)
+had_status_t check_rows(int B, int heads, int T)
 {
     if (B < 1 || T < 1) return HAD_ERR_INVALID_ARG;
     const long long bh = (long long)B * heads;
-    if (bh > INT_MAX || bh * T > INT_MAX) return HAD_ERR_UNSUPPORTED;
-    *rows = (unsigned)(bh * T);
-    return HAD_OK;
+    return bh > INT_MAX || bh * T > INT_MAX ? HAD_ERR_UNSUPPORTED : HAD_OK;
+}
+
+// Rows (b, head, token) of an append or a read, and the grid that has 16
+// lanes for kCacheRows of them.
+CacheTokens tokens_of(const int32_t *table, int max_pages, const int32_t *start,
+                      const int32_t *counts, int B, int heads, int T, unsigned *grid)
+{
+    const unsigned rows = (unsigned)B * heads * T, per = 256 / had::kCacheLanes * had::kCacheRows;
+    *grid = (rows + per - 1) / per;
+    return CacheTokens{table, start, counts, max_pages, T, rows, had::divisor(T),
+                       had::divisor(heads)};
 }
 
 bool finite_nonneg(float x) { return x >= 0.0f && x <= 3.4028234e38f; }
@@ -139,21 +194,20 @@ had_status_t had_cache_append(const void *K, const void *V, had_dtype_t dt, cons
                               int32_t *dev_status, cudaStream_t stream)
 {
     CacheView c;
-    unsigned rows;
     had_status_t s = check_cache(cache, &c);
-    if (s == HAD_OK) s = check_rows(B, c.heads, T, &rows);
+    if (s == HAD_OK) s = check_rows(B, c.heads, T);
     if (s == HAD_OK) s = check_table(table, B, max_pages, cache->page);
     if (s != HAD_OK) return s;
     if (dt != HAD_BF16 && dt != HAD_F32) return HAD_ERR_INVALID_ARG;
     if (!good(K, 16) || !good(V, 16) || !good(sigma_k, 4) || !good(start, 4) ||
         !aligned(counts, 4) || !aligned(dev_status, 4))
         return HAD_ERR_INVALID_ARG;
+    unsigned grid;
+    const CacheTokens k = tokens_of(table, max_pages, start, counts, B, c.heads, T, &grid);
     if (dt == HAD_BF16)
-        launch_append<__nv_bfloat16>(K, V, sigma_k, c, cache->d, table, max_pages, start, counts, T,
-                                     rows, dev_status, stream);
+        launch_append<__nv_bfloat16>(K, V, sigma_k, c, cache->d, k, grid, dev_status, stream);
     else
-        launch_append<float>(K, V, sigma_k, c, cache->d, table, max_pages, start, counts, T, rows,
-                             dev_status, stream);
+        launch_append<float>(K, V, sigma_k, c, cache->d, k, grid, dev_status, stream);
     return launched();
 }
 
@@ -163,22 +217,20 @@ had_status_t had_cache_read(const had_cache_t *cache, const int32_t *table, int 
                             cudaStream_t stream)
 {
     CacheView c;
-    unsigned rows;
     had_status_t s = check_cache(cache, &c);
-    if (s == HAD_OK) s = check_rows(B, c.heads, T, &rows);
+    if (s == HAD_OK) s = check_rows(B, c.heads, T);
     if (s == HAD_OK) s = check_table(table, B, max_pages, cache->page);
     if (s != HAD_OK) return s;
     if (!good(start, 4) || !aligned(counts, 4) || !aligned(bits, 16) || !aligned(values, 16) ||
         !aligned(dev_status, 4))
         return HAD_ERR_INVALID_ARG;
     if (!bits && !values) return HAD_ERR_INVALID_ARG;
-    const unsigned grid = (rows + 15) / 16;
+    unsigned grid;
+    const CacheTokens k = tokens_of(table, max_pages, start, counts, B, c.heads, T, &grid);
     if (cache->d == 64)
-        had::cache_read_kernel<64><<<grid, 256, 0, stream>>>(c, table, max_pages, start, counts, T,
-                                                             rows, bits, values, dev_status);
+        had::cache_read_kernel<64><<<grid, 256, 0, stream>>>(c, k, bits, values, dev_status);
     else
-        had::cache_read_kernel<128><<<grid, 256, 0, stream>>>(c, table, max_pages, start, counts, T,
-                                                              rows, bits, values, dev_status);
+        had::cache_read_kernel<128><<<grid, 256, 0, stream>>>(c, k, bits, values, dev_status);
     return launched();
 }
 
@@ -189,10 +241,9 @@ had_status_t had_cache_attention(const void *Q, had_dtype_t dt, const float *sig
                                  int32_t *dev_status, cudaStream_t stream)
 {
     CacheView c;
-    unsigned rows;
     had_status_t s = check_cache(cache, &c);
     if (s == HAD_OK && Hq < 1) s = HAD_ERR_INVALID_ARG;
-    if (s == HAD_OK) s = check_rows(B, Hq, T, &rows);
+    if (s == HAD_OK) s = check_rows(B, Hq, T);
     if (s == HAD_OK) s = check_table(table, B, max_pages, cache->page);
     if (s != HAD_OK) return s;
     if (Hq % c.heads != 0 || N < 1 || window < 0 || sinks < 0 || !finite_nonneg(tau))
@@ -203,18 +254,11 @@ had_status_t had_cache_attention(const void *Q, had_dtype_t dt, const float *sig
         return HAD_ERR_INVALID_ARG;
     const had::CacheAttnArgs a{Q, sigma_q, c, table, lens, counts, max_pages, Hq, T, N, window,
                                sinks, tau, out, dev_status};
-    if (dt == HAD_BF16) {
-        if (cache->d == 64)
-            had::cache_attn_row_kernel<__nv_bfloat16, 64><<<rows, had::kCacheAttnThreads, 0, stream>>>(a);
-        else
-            had::cache_attn_row_kernel<__nv_bfloat16, 128><<<rows, had::kCacheAttnThreads, 0, stream>>>(a);
-    } else {
-        if (cache->d == 64)
-            had::cache_attn_row_kernel<float, 64><<<rows, had::kCacheAttnThreads, 0, stream>>>(a);
-        else
-            had::cache_attn_row_kernel<float, 128><<<rows, had::kCacheAttnThreads, 0, stream>>>(a);
-    }
-    return launched();
+    if (dt == HAD_BF16)
+        return cache->d == 64 ? launch_attention<__nv_bfloat16, 64>(a, B, stream)
+                              : launch_attention<__nv_bfloat16, 128>(a, B, stream);
+    return cache->d == 64 ? launch_attention<float, 64>(a, B, stream)
+                          : launch_attention<float, 128>(a, B, stream);
 }
 
 had_status_t had_cache_fork(int32_t *table, int32_t *lens, int32_t *refs, int S, int max_pages,

@@ -42,178 +42,300 @@ __device__ __forceinline__ float bf16_down(float x)
     return __uint_as_float(cut);
 }
 
-constexpr int kCacheLanes = 16;        // threads of one (token, head) row
-
-template <typename T, int E>
-__device__ __forceinline__ void load_slice(const T *p, float (&v)[E])
+// min and max that give NaN when an operand is NaN
+__device__ __forceinline__ float min_nan(float a, float b)
 {
-    if constexpr (sizeof(T) == 2 && E == 4) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-        v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
-    } else if constexpr (sizeof(T) == 2) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-        v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
-        v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
-    } else {
-#pragma unroll
-        for (int i = 0; i < E; i += 4) {
-            const float4 f = __ldg(reinterpret_cast<const float4 *>(p + i));
-            v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
-        }
-    }
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-// Position and page of the token `t` of sequence `b`: false where the token
-// is none of the sequence's `count`, or its place is not in the table.
-__device__ __forceinline__ bool cache_place(const CacheView &c, const int32_t *table,
-                                            int max_pages, const int32_t *start,
-                                            const int32_t *counts, int b, int t, int T,
-                                            int &page, int &slot, int32_t *status)
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-    int count = counts ? __ldg(counts + b) : T;
-    if (count < 0 || count > T) {
-        flag(status, HAD_ERR_INVALID_ARG);
-        count = count < 0 ? 0 : T;
-    }
-    if (t >= count) return false;
-    const long long pos = (long long)__ldg(start + b) + t;
-    if (pos < 0 || pos >= (long long)max_pages << c.page_log) {
-        flag(status, HAD_ERR_INVALID_ARG);
-        return false;
-    }
-    page = __ldg(table + (long long)b * max_pages + (pos >> c.page_log));
-    slot = (int)(pos & ((1 << c.page_log) - 1));
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Division of n < 2^31 by a divisor known on the host, with the multiplier
+// m = floor(2^32 (2^s - d) / d) + 1, s = ceil(log2 d): q = (hi(n m) + n) >> s
+// (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994).
+struct Divisor {
+    unsigned d, mul, shift;
+};
+
+inline Divisor divisor(unsigned d)
+{
+    unsigned s = 0;
+    while (s < 31 && (1u << s) < d) ++s;
+    return Divisor{d, (unsigned)((((1ull << s) - d) << 32) / d + 1), s};
+}
+
+__device__ __forceinline__ unsigned divide(unsigned n, const Divisor &d)
+{
+    return (__umulhi(n, d.mul) + n) >> d.shift;
+}
+
+constexpr int kCacheLanes = 16;        // threads of one (token, head) row
+constexpr int kCacheRows = 2;          // rows of a thread whose loads are in flight together
+
+// Where the tokens of an append or a read lie: row i of rows = (b, head, t).
+struct CacheTokens {
+    const int32_t *table, *start, *counts;
+    int max_pages, tokens;
+    unsigned rows;
+    Divisor per_head, heads;
+};
+
+// Row i of them: its sequence, head and token; `real`: one of the sequence's.
+struct CacheToken {
+    int b, head, t;
+    bool real;
+};
+
+__device__ __forceinline__ CacheToken cache_token(const CacheTokens &k, unsigned i, int32_t *status)
+{
+    CacheToken x{0, 0, 0, false};
+    if (i >= k.rows) return x;
+    const unsigned bh = divide(i, k.per_head), b = divide(bh, k.heads);
+    x.b = (int)b;
+    x.head = (int)(bh - b * k.heads.d);
+    x.t = (int)(i - bh * k.per_head.d);
+    const int count = k.counts ? __ldg(k.counts + b) : k.tokens;
+    if (count < 0 || count > k.tokens) flag(status, HAD_ERR_INVALID_ARG);
+    x.real = x.t < count;
+    return x;
+}
+
+// Row of the pool that holds a real token, -1 where the table has no place for it.
+__device__ __forceinline__ long long cache_place(const CacheView &c, const CacheTokens &k,
+                                                 const CacheToken &x, int32_t *status)
+{
+    if (!x.real) return -1;
+    const long long pos = (long long)__ldg(k.start + x.b) + x.t;
+    int page = -1;
+    if (pos >= 0 && pos < (long long)k.max_pages << c.page_log)
+        page = __ldg(k.table + (long long)x.b * k.max_pages + (pos >> c.page_log));
     if (page < 0 || page >= c.pages) {
         flag(status, HAD_ERR_INVALID_ARG);
-        return false;
+        return -1;
     }
-    return true;
+    return cache_row(c, page, x.head, (int)(pos & ((1 << c.page_log) - 1)));
 }
+
+// E = 4 or 8 consecutive elements of a row as one or two 16-byte loads.
+template <typename T, int E>
+struct CacheSlice {
+    static constexpr int kWords = sizeof(T) * E / 4;
+    uint32_t raw[kWords];
+
+    __device__ __forceinline__ void load(const T *p)
+    {
+        if constexpr (kWords == 2) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+            raw[0] = u.x; raw[1] = u.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4);
+                raw[i] = u.x; raw[i + 1] = u.y; raw[i + 2] = u.z; raw[i + 3] = u.w;
+            }
+        }
+    }
+
+    __device__ __forceinline__ float at(int i) const
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(raw[i]);
+        else return i & 1 ? bf16_hi(raw[i / 2]) : bf16_lo(raw[i / 2]);
+    }
+
+    // bit i: element i / sigma < 0 (IEEE fp32)
+    __device__ __forceinline__ uint32_t signs(const SignRule &rule, uint32_t kge) const
+    {
+        uint32_t bits = 0;
+        bool unsure = !rule.fast;
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 2) {
+                uint32_t neg, uns;
+                bf16_signs4(raw[i], raw[i + 1], kge, neg, uns);
+                bits |= flags4(neg) << (2 * i);
+                unsure |= uns != 0u;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                bits |= (uint32_t)(at(i) <= -rule.thr) << i;
+                unsure |= at(i) < 0.0f && at(i) > -rule.thr;
+            }
+        }
+        if (unsure) {
+            bits = 0;
+#pragma unroll
+            for (int i = 0; i < E; ++i) bits |= negative_bit(at(i), rule) << i;
+        }
+        return bits;
+    }
+};
 
 // Tokens into the cache.  Signs: x / sigma < 0 (IEEE fp32), packed.  Values,
 // all steps in IEEE fp32: z = the row's minimum rounded down to bf16, s = the
 // quotient (max - z) / 15 rounded up to bf16, c = (v - z) / s rounded to the
-// nearest whole number (even on ties) and clamped to [0, 15]; s and z are
-// rounded outwards so that no value lies beyond code 15 by more than the
-// rounding of the quotient.  s = 0 (a constant row that bf16 holds) gives
-// codes 0.  A row with a NaN or an infinity, or whose z, s or range is not
-// finite, gets s = z = NaN and codes 0: whoever keeps it sees NaN.
+// nearest whole number (even on ties); s and z are rounded outwards, so a
+// quotient lies in [0, 15 (1 + 2^-23)] and needs no clamp.  s = 0 (a constant
+// row that bf16 holds) gives codes 0.  A row with a NaN or an infinity, or
+// whose z or 15 s is not finite, gets s = z = NaN and codes 0: whoever keeps
+// it sees NaN.
 //
-// HBM-bound: 2 d elements read, d/8 + d/2 + 4 bytes written per row.  16
-// lanes take a row, so that a bf16 row of d = 128 is one 16-byte load per
-// lane; the extremes are joined by four shuffles and a word of signs by the
-// 32 / E lanes that hold its elements (E = d / 16 elements per lane).
+// HBM-bound once the arithmetic is lean: 2 d elements read, d/8 + d/2 + 4
+// bytes written per row.  16 lanes take a row, so that a bf16 row of d = 128
+// is one 16-byte load per lane, and two rows are in flight; the extremes are
+// joined by four shuffles and a word of signs by the 32 / E lanes that hold its
+// elements (E = d / 16).  The quotients are products with 1 / s (off by less
+// than 2^-18 in all: three roundings of at most 16) and only a slice with one
+// that close to a half divides.  No lane leaves early: the shuffles then name
+// the whole warp, and half-warp masks cost more than all of the arithmetic
+// (measured on 197 k rows of d 128, bf16, with the exact divisions: 80 us
+// against APPEND_US now, 22 us of HBM time).
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
 cache_append_kernel(const T *__restrict__ K, const T *__restrict__ V,
-                    const float *__restrict__ sigma, CacheView c,
-                    const int32_t *__restrict__ table, int max_pages,
-                    const int32_t *__restrict__ start, const int32_t *__restrict__ counts,
-                    int tokens, unsigned rows, int32_t *status)
+                    const float *__restrict__ sigma, CacheView c, CacheTokens k, int32_t *status)
 {
-    constexpr int E = D / kCacheLanes;
-    const int lane = threadIdx.x & 31;
-    const int l = lane & (kCacheLanes - 1);
-    const unsigned row = (blockIdx.x * 256u + threadIdx.x) / kCacheLanes;
-    const unsigned half = 0xffffu << (lane & 16);     // the lanes of this row
-    if (row >= rows) return;
-    const unsigned bh = row / (unsigned)tokens;
-    const int t = (int)(row - bh * (unsigned)tokens);
-    const int b = (int)(bh / (unsigned)c.heads), h = (int)(bh - (unsigned)b * c.heads);
-    const SignRule rule = sign_rule(__ldg(sigma + h));
-    if (rule.bad && l == 0) flag(status, HAD_ERR_BAD_SIGMA);
-    int page, slot;
-    if (!cache_place(c, table, max_pages, start, counts, b, t, tokens, page, slot, status)) return;
-    const long long at = cache_row(c, page, h, slot);
-    const long long from = (long long)row * D + l * E;
-    float k[E], v[E];
-    load_slice<T, E>(K + from, k);
-    load_slice<T, E>(V + from, v);
-
-    uint32_t word = 0;
+    constexpr int E = D / kCacheLanes, kPerWord = 32 / E;
+    const int l = threadIdx.x & (kCacheLanes - 1);
+    const unsigned step = gridDim.x * (256u / kCacheLanes);
+    const unsigned row0 = (blockIdx.x * 256u + threadIdx.x) / kCacheLanes;
+    CacheSlice<T, E> key[kCacheRows], value[kCacheRows];
+    CacheToken token[kCacheRows];
+    long long at[kCacheRows];
+    float sg[kCacheRows];
 #pragma unroll
-    for (int i = 0; i < E; ++i) word |= negative_bit(k[i], rule) << i;
-    constexpr int kPerWord = 32 / E;
-    word <<= E * (l & (kPerWord - 1));
+    for (int i = 0; i < kCacheRows; ++i) token[i] = cache_token(k, row0 + i * step, status);
 #pragma unroll
-    for (int o = 1; o < kPerWord; o <<= 1) word |= __shfl_xor_sync(half, word, o);
-    if ((l & (kPerWord - 1)) == 0) c.kbits[at * (D / 32) + l / kPerWord] = word;
-
-    float lo = v[0], hi = v[0];
-    bool fine = true;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        fine &= fabsf(v[i]) <= FLT_MAX;
-        lo = fminf(lo, v[i]);
-        hi = fmaxf(hi, v[i]);
+    for (int i = 0; i < kCacheRows; ++i) {
+        // (a token that is not there reads the first row: it is in the cache)
+        const long long row = token[i].real ? row0 + i * step : 0;
+        key[i].load(K + row * D + l * E);
+        value[i].load(V + row * D + l * E);
+        sg[i] = __ldg(sigma + token[i].head);
     }
 #pragma unroll
-    for (int o = 1; o < kCacheLanes; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(half, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(half, hi, o));
-    }
-    fine = __all_sync(half, fine);
-    const float z = bf16_down(lo + 0.0f);             // -0 becomes +0
-    const float s = -bf16_down(-__fdiv_rn(hi - z, 15.0f)) + 0.0f;
-    fine &= fabsf(z) <= FLT_MAX && 15.0f * s <= FLT_MAX;
-    uint32_t codes = 0;
-    if (fine && s > 0.0f) {
+    for (int i = 0; i < kCacheRows; ++i) at[i] = cache_place(c, k, token[i], status);
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float q = rintf(__fdiv_rn(v[i] - z, s));
-            codes |= (uint32_t)fminf(fmaxf(q, 0.0f), 15.0f) << (4 * i);
+    for (int i = 0; i < kCacheRows; ++i) {
+        const bool here = at[i] >= 0;
+        const SignRule rule = sign_rule(sg[i]);
+        if (rule.bad && l == 0 && here) flag(status, HAD_ERR_BAD_SIGMA);
+        uint32_t word = key[i].signs(rule, bf16_kge(rule)) << (E * (l & (kPerWord - 1)));
+#pragma unroll
+        for (int o = 1; o < kPerWord; o <<= 1) word |= __shfl_xor_sync(kFullMask, word, o);
+        if (here && (l & (kPerWord - 1)) == 0) c.kbits[at[i] * (D / 32) + l / kPerWord] = word;
+
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = value[i].at(e);
+        float lo = v[0], hi = v[0];
+#pragma unroll
+        for (int e = 1; e < E; ++e) {
+            lo = min_nan(lo, v[e]);
+            hi = max_nan(hi, v[e]);
+        }
+#pragma unroll
+        for (int o = 1; o < kCacheLanes; o <<= 1) {
+            lo = min_nan(lo, __shfl_xor_sync(kFullMask, lo, o));
+            hi = max_nan(hi, __shfl_xor_sync(kFullMask, hi, o));
+        }
+        const float z = bf16_down(lo + 0.0f);         // -0 becomes +0
+        const float s = -bf16_down(-__fdiv_rn(hi - z, 15.0f)) + 0.0f;
+        const bool fine = fabsf(lo) <= FLT_MAX && fabsf(hi) <= FLT_MAX && fabsf(z) <= FLT_MAX &&
+                          15.0f * s <= FLT_MAX;
+        const bool coded = fine && s > 0.0f;
+        const float inv = __frcp_rn(s);
+        // four codes c0 + 16 c1 + 256 c2 + 4096 c3 are a whole number below
+        // 2^16, exact in fp32, and the last bits of its sum with 2^23
+        constexpr float kWhole = 12582912.0f;         // 1.5 2^23: the sum's last bit is 1
+        float far = 0.0f;
+        uint32_t codes = 0;
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+            float four = 0.0f;
+#pragma unroll
+            for (int f = 3; f >= 0; --f) {
+                const float q = (v[e + f] - z) * inv, r = (q + kWhole) - kWhole;
+                far = fmaxf(far, fabsf(q - r));
+                four = fmaf(four, 16.0f, r);
+            }
+            codes |= (__float_as_uint(four + 8388608.0f) & 0xffffu) << (4 * e);
+        }
+        // 1 / s overflows below 2^-128: such rows divide, too
+        if (coded && (!(far < 0.5f - 7.6293945e-6f) || !(inv <= FLT_MAX))) {
+            codes = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) codes |= (uint32_t)rintf(__fdiv_rn(v[e] - z, s)) << (4 * e);
+        }
+        if (!coded) codes = 0;
+        if (here) {
+            if constexpr (E == 8)
+                reinterpret_cast<uint32_t *>(c.vcodes)[at[i] * kCacheLanes + l] = codes;
+            else
+                reinterpret_cast<uint16_t *>(c.vcodes)[at[i] * kCacheLanes + l] = (uint16_t)codes;
+            if (l == 0)
+                c.vscale[at[i]] = fine ? (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xffff0000u)
+                                       : 0x7fc07fc0u;
         }
     }
-    if constexpr (E == 8)
-        reinterpret_cast<uint32_t *>(c.vcodes)[at * kCacheLanes + l] = codes;
-    else
-        reinterpret_cast<uint16_t *>(c.vcodes)[at * kCacheLanes + l] = (uint16_t)codes;
-    if (l == 0)
-        c.vscale[at] = fine ? (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xffff0000u)
-                            : 0x7fc07fc0u;
 }
 
 // Tokens of the cache as packed signs and fp32 values c s + z (one FMA:
 // rounded once); zeros for tokens beyond a sequence's count.  HBM-bound by
-// the 4 d bytes written per row; 16 lanes a row, each one load of codes and
-// 16-byte stores.
+// the 4 d bytes written per row; 16 lanes a row, each E / 4 times 16 bytes of
+// consecutive lanes, two rows in flight (READ_US for 262 k rows of d 128, of
+// which 197 k are there; 23 us of HBM time).
 template <int D>
 __global__ void __launch_bounds__(256)
-cache_read_kernel(CacheView c, const int32_t *__restrict__ table, int max_pages,
-                  const int32_t *__restrict__ start, const int32_t *__restrict__ counts,
-                  int tokens, unsigned rows, uint32_t *__restrict__ bits,
+cache_read_kernel(CacheView c, CacheTokens k, uint32_t *__restrict__ bits,
                   float *__restrict__ values, int32_t *status)
 {
     constexpr int E = D / kCacheLanes;
     const int l = threadIdx.x & (kCacheLanes - 1);
-    const unsigned row = (blockIdx.x * 256u + threadIdx.x) / kCacheLanes;
-    if (row >= rows) return;
-    const unsigned bh = row / (unsigned)tokens;
-    const int t = (int)(row - bh * (unsigned)tokens);
-    const int b = (int)(bh / (unsigned)c.heads), h = (int)(bh - (unsigned)b * c.heads);
-    int page, slot;
-    const bool have = cache_place(c, table, max_pages, start, counts, b, t, tokens, page, slot, status);
-    const long long at = have ? cache_row(c, page, h, slot) : 0;
-    if (bits && l < D / 32) bits[(long long)row * (D / 32) + l] = have ? c.kbits[at * (D / 32) + l] : 0u;
-    if (!values) return;
-    uint32_t codes = 0, sz = 0;
-    if (have) {
-        if constexpr (E == 8)
-            codes = reinterpret_cast<const uint32_t *>(c.vcodes)[at * kCacheLanes + l];
-        else
-            codes = reinterpret_cast<const uint16_t *>(c.vcodes)[at * kCacheLanes + l];
-        sz = c.vscale[at];
-    }
-    const float s = bf16_lo(sz), z = bf16_hi(sz);
-    float4 *out = reinterpret_cast<float4 *>(values + (long long)row * D + l * E);
+    const unsigned step = gridDim.x * (256u / kCacheLanes);
+    const unsigned row0 = (blockIdx.x * 256u + threadIdx.x) / kCacheLanes;
+    long long at[kCacheRows];
+    uint32_t codes[kCacheRows][E / 4], sz[kCacheRows], word[kCacheRows];
 #pragma unroll
-    for (int i = 0; i < E; i += 4) {
-        float4 f;
-        f.x = fmaf((float)(codes >> (4 * i) & 15u), s, z);
-        f.y = fmaf((float)(codes >> (4 * i + 4) & 15u), s, z);
-        f.z = fmaf((float)(codes >> (4 * i + 8) & 15u), s, z);
-        f.w = fmaf((float)(codes >> (4 * i + 12) & 15u), s, z);
-        out[i / 4] = f;
+    for (int i = 0; i < kCacheRows; ++i) {
+        const unsigned row = row0 + i * step;
+        at[i] = cache_place(c, k, cache_token(k, row, status), status);
+    }
+#pragma unroll
+    for (int i = 0; i < kCacheRows; ++i) {
+        const bool here = at[i] >= 0;
+        word[i] = here && bits && l < D / 32 ? __ldg(c.kbits + at[i] * (D / 32) + l) : 0u;
+        sz[i] = here && values ? __ldg(c.vscale + at[i]) : 0u;
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e)
+            codes[i][e] = here && values ? __ldg(reinterpret_cast<const uint16_t *>(c.vcodes) +
+                                                 at[i] * (D / 4) + e * kCacheLanes + l) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < kCacheRows; ++i) {
+        const unsigned row = row0 + i * step;
+        if (row >= k.rows) break;
+        if (bits && l < D / 32) bits[(long long)row * (D / 32) + l] = word[i];
+        if (!values) continue;
+        const float s = bf16_lo(sz[i]), z = bf16_hi(sz[i]);
+        // 2^23 + c has c in its last bits
+        auto value = [&](uint32_t code) {
+            return fmaf(__uint_as_float((code & 15u) | 0x4b000000u) - 8388608.0f, s, z);
+        };
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e) {
+            const uint32_t x = codes[i][e];
+            float4 f = make_float4(value(x), value(x >> 4), value(x >> 8), value(x >> 12));
+            reinterpret_cast<float4 *>(values + (long long)row * D)[e * kCacheLanes + l] = f;
+        }
     }
 }
 

@@ -8,11 +8,36 @@
 //   out = sum_kept p_j (c_j s_j + z_j),  p = softmax(tau (d - 2 h)) over them.
 // A logit is one of d + 1 levels, so the row's histogram of distances gives
 // the threshold level, the ties kept on it, the largest logit and the sum Z
-// of the softmax; a second pass over the keys takes the values.
+// of the softmax before any value is read: p_j is a table lookup by h_j, and
+// partial sums over parts of the keys just add up.
+//
+// One cluster of CTAs takes a tile of R rows that share a key-value head (its
+// query heads, and neighbouring tokens of a draft or chunk) and splits the keys
+// that any of them sees; a CTA's eight warps split its slice, in key order.
+//   1. Distances: a lane per key, the key's bits in registers, XOR + popc with
+//      every row's bits from shared memory; 8-bit distances stay in shared
+//      memory (255: not visible), counts go to the CTA's histograms.
+//   2. The cluster's histograms are read through distributed shared memory; a
+//      warp per row finds level, quota and Z and fills p[h].  The ties that
+//      lower-ranked CTAs hold come from the same counts.
+//   3. Each warp drops what its rows do not keep (ties by rank in key order)
+//      and moves the keys that at least one row keeps to the front of its part.
+//   4. Per 16 listed keys: the tile's P V on the tensor core.  The codes are
+//      whole numbers below 16, exact in bf16; the weights p s are fp32 and are
+//      cut into three bf16 terms, which hold all 24 bits, and stacked as rows
+//      of A: row x = term R + r.  So the product is as exact as fp32 and any
+//      scale keeps its exponent.  The product takes c - 8 in place of c; the
+//      rest, p (z + 8 s), is summed beside it.
+//   5. Warps, terms and CTAs are added in a fixed order.
+// The union of the rows' kept keys is read once, each key's bits once.
 #pragma once
+#include <cooperative_groups.h>
+
 #include "had_cache.cuh"
 
 namespace had {
+
+namespace cg = cooperative_groups;
 
 struct CacheAttnArgs {
     const void *Q;
@@ -25,9 +50,7 @@ struct CacheAttnArgs {
     int32_t *status;
 };
 
-constexpr int kCacheAttnThreads = 256;
-
-// Visible range of a row: keys [0, sinks) and [lo, pos], pos = -1 for none.
+// Visible keys of a row: [0, sinks) and [lo, pos]; pos = -1 for none.
 struct RowRange {
     int sinks, lo, pos;
 };
@@ -35,139 +58,617 @@ struct RowRange {
 __device__ __forceinline__ RowRange row_range(const CacheAttnArgs &a, int len, int count, int t)
 {
     RowRange r;
-    r.pos = t < count ? len - count + t : -1;
-    if (r.pos < 0) r.pos = -1;
+    r.pos = t < count ? max(len - count + t, -1) : -1;
     r.lo = a.window > 0 ? max(0, r.pos - a.window + 1) : 0;
     r.sinks = min(a.sinks, r.lo);
     return r;
 }
 
-// One CTA per row: distances and histogram, threshold, then the kept tokens
-// 256 at a time.
-template <typename T, int D>
-__global__ void __launch_bounds__(kCacheAttnThreads)
-cache_attn_row_kernel(CacheAttnArgs a)
+constexpr int kCacheAttnThreads = 256;
+constexpr int kCacheAttnWarps = kCacheAttnThreads / 32;
+constexpr uint32_t kUnseen = 255u;     // distance byte of a key that a row does not keep
+
+// Rows of a tile: three terms each in NA tiles of 16 stacked rows.
+__host__ __device__ constexpr int cache_attn_rows(int na) { return na * 16 / 3; }
+
+// The tile's split: R rows, `tiles` tiles per (sequence, head), `ctas` per
+// cluster, `cap` keys a CTA holds at once (a multiple of 256).
+struct CacheAttnPlan {
+    int R, tiles, ctas, cap;
+};
+
+// Entries of the list of pages under `cap` keys: two runs of keys (the first
+// tokens and the window) that need not begin with a page.
+__host__ __device__ constexpr int cache_attn_pages(int cap) { return cap / 16 + 4; }
+
+// A warp's own shared memory in step 4: a ring of kStages chunks of 16 keys
+// (codes, rows padded by 16 bytes so that the eight lanes of a key and the four
+// keys of a load fall on different banks; scales), and the stacked rows of A.
+constexpr int kStages = 4;
+
+template <int D, int NA>
+struct WarpStage {
+    static constexpr int kStride = D / 2 + 16;
+    __align__(16) unsigned char codes[kStages][16 * kStride];
+    __align__(8) uint32_t scale[kStages][16];
+    __align__(16) uint32_t terms[16 * NA][8];        // bf16 of two neighbouring keys
+};
+
+// Bytes of shared memory of a key: its row in the pool, a distance per row.
+__host__ __device__ constexpr int cache_attn_key_bytes(int R) { return 4 + (R + 3) / 4 * 4; }
+
+// Floats of the cross-warp sums: accumulators and p z of one warp, per lane.
+template <int D, int NA>
+constexpr int cache_attn_red_regs()
+{
+    return NA * D / 2 + (cache_attn_rows(NA) + 3) / 4;
+}
+
+template <int D, int NA>
+size_t cache_attn_smem_bytes(const CacheAttnPlan &p)
+{
+    const size_t keys = sizeof(WarpStage<D, NA>) * kCacheAttnWarps +
+                        (size_t)p.cap * cache_attn_key_bytes(p.R) + cache_attn_pages(p.cap) * 4;
+    const size_t red = kCacheAttnWarps / 2 * 32 * 4 * cache_attn_red_regs<D, NA>();
+    return keys > red ? keys : red;
+}
+
+__device__ __forceinline__ void copy_async16(void *to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+
+__device__ __forceinline__ void copy_async4(void *to, const void *from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                 :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+                 "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Codes of four bits of two keys (16-bit halves of x) as bf16 c - 8: 128 + c
+// has c in its last mantissa bits, and 136 is taken off exactly.  The tensor
+// core cuts its running sums, it does not round them; sums of the centred
+// codes stay near zero, those of c itself would grow with every key and lose
+// bits on the way (16 k keys, N 2048: relative error 3.3e-6 instead of
+// CENTRED).
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t x)
+{
+    const uint32_t biased = (x & 0x000f000fu) | 0x43004300u;
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(biased), "r"(0x43084308u));
+    return r;
+}
+
+template <int D, int NA>
+struct CacheAttnShared {
+    static constexpr int RM = cache_attn_rows(NA);
+    __align__(16) uint32_t qbits[RM][D / 32];
+    int pos[RM], lo[RM];
+    int hist[RM][D + 1];
+    float p[RM][D + 1];
+    int level[RM], quota[RM];
+    int ties[kCacheAttnWarps][RM];
+    float zsum[RM];
+    float part[RM][D];
+};
+
+template <typename T, int D, int NA>
+__global__ void __launch_bounds__(kCacheAttnThreads, NA * D <= 128 ? 2 : 1)
+cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 {
     constexpr int DW = D / 32;
-    constexpr int kWarps = kCacheAttnThreads / 32;
-    constexpr int kParts = kCacheAttnThreads / (D / 2);
-    __shared__ uint32_t qbits[DW];
-    __shared__ int hist[D + 1];
-    __shared__ float weight[D + 1];
-    __shared__ int level, quota, warp_ties[kWarps], warp_kept[kWarps];
-    __shared__ long long kept_row[kCacheAttnThreads];
-    __shared__ float kept_p[kCacheAttnThreads];
-    __shared__ float sums[kParts][D];
-
+    constexpr int kTiles = D / 8;             // 8-wide column tiles of the value
+    constexpr int kCodeWords = D / 64;        // 32-bit words of codes per lane and key
+    constexpr int RWM = (cache_attn_rows(NA) + 3) / 4;        // most words of four row bytes
+    constexpr uint32_t kNoRow = 0xffffffffu;
+    constexpr int KU = 4;                     // keys per lane of one step of the distances
+    using Shared = CacheAttnShared<D, NA>;
+    extern __shared__ __align__(16) unsigned char attn_smem[];
+    __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long row = blockIdx.x;
-    const int t = (int)(row % a.T);
-    const int hq = (int)(row / a.T % a.Hq), b = (int)(row / a.T / a.Hq);
-    const int h = hq / (a.Hq / a.c.heads);
-    const int32_t *table = a.table + (long long)b * a.max_pages;
-    int len = a.lens[b], count = a.counts ? a.counts[b] : a.T;
-    if (len < 0 || len > (long long)a.max_pages << a.c.page_log || count < 0 || count > a.T) {
+    const int R = plan.R, RW = (R + 3) / 4, cap = plan.cap;
+    using Stage = WarpStage<D, NA>;
+    Stage &stage = reinterpret_cast<Stage *>(attn_smem)[warp];
+    uint32_t *const distw = reinterpret_cast<uint32_t *>(                    // [RW][cap]
+        attn_smem + sizeof(Stage) * kCacheAttnWarps);
+    uint32_t *const pool_row = distw + RW * cap;                             // [cap]
+    int *const page_of = reinterpret_cast<int *>(pool_row + cap);
+
+    const int C = plan.ctas;
+    const int rank = (int)(blockIdx.x % (unsigned)C);
+    const unsigned unit = blockIdx.x / (unsigned)C;
+    const int tile = (int)(unit % (unsigned)plan.tiles);
+    const unsigned bh = unit / (unsigned)plan.tiles;
+    const int h = (int)(bh % (unsigned)a.c.heads), b = (int)(bh / (unsigned)a.c.heads);
+    const int G = a.Hq / a.c.heads;
+    const int row0 = tile * R, rows = min(R, G * a.T - row0);
+    const int lg = a.c.page_log, page_mask = (1 << lg) - 1;
+    const int32_t *const table = a.table + (long long)b * a.max_pages;
+
+    int len = __ldg(a.lens + b), count = a.counts ? __ldg(a.counts + b) : a.T;
+    if (len < 0 || len > (long long)a.max_pages << lg || count < 0 || count > a.T) {
         if (tid == 0) flag(a.status, HAD_ERR_INVALID_ARG);
         len = count = 0;
     }
-    const RowRange rr = row_range(a, len, count, t);
-    const int total = rr.pos < 0 ? 0 : rr.sinks + rr.pos + 1 - rr.lo;
 
-    const SignRule rule = sign_rule(a.sigma[hq]);
-    if (tid < D) {
-        if (rule.bad && tid == 0) flag(a.status, HAD_ERR_BAD_SIGMA);
-        const float x = (float)static_cast<const T *>(a.Q)[row * D + tid];
-        const uint32_t w = __ballot_sync(kFullMask, negative_bit(x, rule));
-        if (lane == 0) qbits[warp] = w;
-    }
-    for (int l = tid; l <= D; l += kCacheAttnThreads) hist[l] = 0;
-    __syncthreads();
-
-    // row of key u of the visible ones, or -1 where the table holds no page
-    auto place = [&](int u) -> long long {
-        const int j = u < rr.sinks ? u : u - rr.sinks + rr.lo;
-        const int page = table[j >> a.c.page_log];
-        if (page < 0 || page >= a.c.pages) return -1;
-        return cache_row(a.c, page, h, j & ((1 << a.c.page_log) - 1));
+    // row r of the tile: token (row0 + r) / G, query head h G + (row0 + r) % G
+    auto q_row = [&](int r) -> long long {
+        const int t = (row0 + r) / G, g = (row0 + r) % G;
+        return ((long long)b * a.Hq + h * G + g) * a.T + t;
     };
-    auto distance = [&](long long at) -> int {
-        int n = 0;
+    for (int r = warp; r < rows; r += kCacheAttnWarps) {
+        const long long at = q_row(r) * D;
+        const SignRule rule = sign_rule(__ldg(a.sigma + h * G + (row0 + r) % G));
+        if (rule.bad && lane == 0) flag(a.status, HAD_ERR_BAD_SIGMA);
 #pragma unroll
-        for (int w = 0; w < DW; ++w) n += __popc(a.c.kbits[at * DW + w] ^ qbits[w]);
-        return n;
-    };
-    for (int u = tid; u < total; u += kCacheAttnThreads) {
-        const long long at = place(u);
-        if (at < 0)
-            flag(a.status, HAD_ERR_INVALID_ARG);
-        else
-            atomicAdd(&hist[distance(at)], 1);
-    }
-    __syncthreads();
-    if (tid == 0) {
-        int first = -1, seen = 0, l = 0;
-        float z = 0.0f;
-        level = -1;
-        quota = 0;
-        for (; l <= D && seen < a.N; ++l) {
-            weight[l] = 0.0f;
-            if (hist[l] == 0) continue;
-            if (first < 0) first = l;
-            const int n = min(hist[l], a.N - seen);
-            weight[l] = expf(a.tau * (float)(2 * (first - l)));
-            z += (float)n * weight[l];
-            seen += n;
-            level = l;
-            quota = n;
+        for (int w = 0; w < DW; ++w) {
+            const float x = (float)static_cast<const T *>(a.Q)[at + 32 * w + lane];
+            const uint32_t word = __ballot_sync(kFullMask, negative_bit(x, rule));
+            if (lane == 0) sh.qbits[r][w] = word;
         }
-        for (int k = 0; k <= level; ++k) weight[k] /= z;
+        if (lane == 0) {
+            const RowRange rr = row_range(a, len, count, (row0 + r) / G);
+            sh.pos[r] = rr.pos;
+            sh.lo[r] = rr.lo;
+        }
+    }
+    for (int i = tid; i < R * (D + 1); i += kCacheAttnThreads) (&sh.hist[0][0])[i] = 0;
+
+    // keys that some row of the tile sees: [0, first_n) and [lo, hi]
+    const int t_lo = max(row0 / G, count - len), t_hi = min((row0 + rows - 1) / G, count - 1);
+    int lo = 0, first_n = 0, total = 0;
+    int min_pos = -1, max_lo = 0;             // a key in [max_lo, min_pos] is seen by every row
+    if (t_lo <= t_hi) {
+        const RowRange from = row_range(a, len, count, t_lo), to = row_range(a, len, count, t_hi);
+        lo = from.lo;
+        first_n = from.sinks;
+        total = first_n + to.pos + 1 - lo;
+        max_lo = to.lo;
+        if (row0 / G == t_lo && (row0 + rows - 1) / G == t_hi) min_pos = from.pos;
+    }
+    const int first_pages = (first_n + page_mask) >> lg;
+    // this CTA's slice of them, whole groups of 32
+    const int per = ((total + C - 1) / C + 31) & ~31;
+    const int u0 = min(total, rank * per), u1 = min(total, u0 + per);
+    const int segs = max(1, (u1 - u0 + cap - 1) / cap);
+
+    auto key_of = [&](int u) { return u < first_n ? u : u - first_n + lo; };
+    auto page_at = [&](int u) {               // index of u's page among the pages of all keys
+        return u < first_n ? u >> lg : ((u - first_n + lo) >> lg) - (lo >> lg) + first_pages;
+    };
+    // Keys s0 .. s0 + n - 1 of the slice: their pages, then this warp's distances.
+    auto load_pages = [&](int s0, int n) {
+        if (n <= 0) return;
+        const int first = page_at(s0), last = page_at(s0 + n - 1);
+        for (int i = first + tid; i <= last; i += kCacheAttnThreads) {
+            int page = __ldg(table + (i < first_pages ? i : i - first_pages + (lo >> lg)));
+            if (page < 0 || page >= a.c.pages) {
+                flag(a.status, HAD_ERR_INVALID_ARG);
+                page = -1;
+            }
+            page_of[i - first] = page;
+        }
+    };
+    auto distances = [&](int s0, int wb, int we, bool with_hist) {
+        if (wb >= we) return;
+        const int page0 = page_at(s0);
+        uint32_t next[KU][DW], next_row[KU];
+        auto fetch = [&](int k0) {
+#pragma unroll
+            for (int i = 0; i < KU; ++i) {
+                const int k = k0 + 32 * i + lane, u = min(s0 + k, s0 + we - 1);
+                const int page = page_of[page_at(u) - page0];
+                const bool have = k < we && page >= 0;
+                next_row[i] = have ? (uint32_t)(((page * (unsigned)a.c.heads + h) << lg) +
+                                                (key_of(u) & page_mask)) : kNoRow;
+#pragma unroll
+                for (int w = 0; w < DW; ++w) next[i][w] = 0u;
+                if (have) {
+                    if constexpr (DW == 2) {
+                        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(a.c.kbits) + next_row[i]);
+                        next[i][0] = x.x; next[i][1] = x.y;
+                    } else {
+                        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a.c.kbits) + next_row[i]);
+                        next[i][0] = x.x; next[i][1] = x.y; next[i][2] = x.z; next[i][3] = x.w;
+                    }
+                }
+            }
+        };
+        // 32 KU keys against all rows; `mixed`: some row may not see some key
+        auto step = [&](int k0, const uint32_t (&bits)[KU][DW], const uint32_t (&at)[KU], bool mixed) {
+            for (int q = 0; q < RW; ++q) {
+                uint32_t word[KU];
+#pragma unroll
+                for (int i = 0; i < KU; ++i) word[i] = 0xffffffffu;
+#pragma unroll
+                for (int rr = 0; rr < 4; ++rr) {
+                    const int r = 4 * q + rr;
+                    if (r >= rows) break;
+                    uint32_t qb[DW];
+                    if constexpr (DW == 2) {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(sh.qbits[r]);
+                        qb[0] = x.x; qb[1] = x.y;
+                    } else {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(sh.qbits[r]);
+                        qb[0] = x.x; qb[1] = x.y; qb[2] = x.z; qb[3] = x.w;
+                    }
+                    const int pos = mixed ? sh.pos[r] : 0, row_lo = mixed ? sh.lo[r] : 0;
+#pragma unroll
+                    for (int i = 0; i < KU; ++i) {
+                        int n = 0;
+#pragma unroll
+                        for (int w = 0; w < DW; ++w) n += __popc(bits[i][w] ^ qb[w]);
+                        bool vis = at[i] != kNoRow;
+                        if (mixed) {
+                            const int key = key_of(s0 + k0 + 32 * i + lane);
+                            vis = vis && key <= pos && (key >= row_lo || key < a.sinks);
+                        }
+                        if (vis) {
+                            word[i] ^= (kUnseen ^ (uint32_t)n) << (8 * rr);
+                            if (with_hist) atomicAdd(&sh.hist[r][n], 1);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < KU; ++i) {
+                    const int k = k0 + 32 * i + lane;
+                    if (k < we) distw[q * cap + k] = word[i];
+                }
+            }
+        };
+        fetch(wb);
+        for (int k0 = wb; k0 < we; k0 += 32 * KU) {
+            uint32_t bits[KU][DW], at[KU];
+#pragma unroll
+            for (int i = 0; i < KU; ++i) {
+                at[i] = next_row[i];
+                if (k0 + 32 * i + lane < we) pool_row[k0 + 32 * i + lane] = at[i];
+#pragma unroll
+                for (int w = 0; w < DW; ++w) bits[i][w] = next[i][w];
+            }
+            if (k0 + 32 * KU < we) fetch(k0 + 32 * KU);
+            const int k_last = min(we, k0 + 32 * KU) - 1;
+            if (key_of(s0 + k_last) <= min_pos && key_of(s0 + k0) >= max_lo)
+                step(k0, bits, at, false);
+            else
+                step(k0, bits, at, true);
+        }
+    };
+    // a warp's part of n keys: whole groups of 32, in key order
+    auto warp_begin = [&](int n, int w) { return min(n, w * (((n + 255) / 256) * 32)); };
+
+    for (int seg = 0; seg < segs; ++seg) {
+        const int s0 = u0 + seg * cap, n = min(cap, u1 - s0);
+        __syncthreads();                      // rows are set up; the last segment's pages are done
+        load_pages(s0, n);
+        __syncthreads();
+        distances(s0, warp_begin(n, warp), warp_begin(n, warp + 1), true);
+    }
+    cg::cluster_group cluster = cg::this_cluster();
+    if (C > 1) cluster.sync();
+    else __syncthreads();
+
+    // level, quota and weights: a warp per row, EL consecutive levels per lane
+    for (int r = warp; r < rows; r += kCacheAttnWarps) {
+        constexpr int EL = (D + 1 + 31) / 32;
+        int cnt[EL], before[EL], sum = 0;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) cnt[e] = before[e] = 0;
+        for (int o = 0; o < C; ++o) {
+            const int *hist = C > 1 ? cluster.map_shared_rank(&sh.hist[r][0], o) : &sh.hist[r][0];
+#pragma unroll
+            for (int e = 0; e < EL; ++e) {
+                const int l = lane * EL + e;
+                const int x = l <= D ? hist[l] : 0;
+                cnt[e] += x;
+                before[e] += o < rank ? x : 0;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < EL; ++e) sum += cnt[e];
+        int upto = sum;                       // inclusive prefix over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kFullMask, upto, o);
+            if (lane >= o) upto += x;
+        }
+        const int seen = __shfl_sync(kFullMask, upto, 31), n = min(a.N, seen);
+        int cum = upto - sum, level = -1, quota = 0, first = D + 1;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+            if (cnt[e] > 0 && first > D) first = lane * EL + e;
+            if (cum < n && n <= cum + cnt[e]) {
+                level = lane * EL + e;
+                quota = n - cum;
+                sh.quota[r] = max(0, quota - before[e]);
+            }
+            cum += cnt[e];
+        }
+        first = __reduce_min_sync(kFullMask, first);
+        const int owner = __reduce_max_sync(kFullMask, level >= 0 ? lane : -1);
+        level = __shfl_sync(kFullMask, level, max(owner, 0));
+        quota = __shfl_sync(kFullMask, quota, max(owner, 0));
+        float w[EL], z = 0.0f;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+            const int l = lane * EL + e;
+            w[e] = l <= level && cnt[e] > 0 ? expf(a.tau * (float)(2 * (first - l))) : 0.0f;
+            z += w[e] * (float)(l < level ? cnt[e] : quota);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFullMask, z, o);
+#pragma unroll
+        for (int e = 0; e < EL; ++e)
+            if (lane * EL + e <= D) sh.p[r][lane * EL + e] = z > 0.0f ? w[e] / z : 0.0f;
+        if (lane == 0) {
+            sh.level[r] = level;
+            if (level < 0) sh.quota[r] = 0;
+        }
     }
     __syncthreads();
 
-    const int t_level = level;
-    int t_quota = quota;
-    const int pair = tid % (D / 2), part = tid / (D / 2);
-    float acc0 = 0.0f, acc1 = 0.0f;
-    for (int u0 = 0; u0 < total; u0 += kCacheAttnThreads) {
-        const long long at = u0 + tid < total ? place(u0 + tid) : -1;
-        const int dist = at >= 0 ? distance(at) : D + 1;
-        const unsigned ties = __ballot_sync(kFullMask, dist == t_level);
-        if (lane == 0) warp_ties[warp] = __popc(ties);
-        __syncthreads();
-        int before = __popc(ties & ((1u << lane) - 1)), all = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            before += w < warp ? warp_ties[w] : 0;
-            all += warp_ties[w];
+    const int g = lane >> 2, t4 = lane & 3;
+    float acc[NA][kTiles][4], zacc[RWM];
+#pragma unroll
+    for (int m = 0; m < NA; ++m)
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][i][e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < RWM; ++i) zacc[i] = 0.0f;
+    // stacked rows that no term fills stay zero
+    for (int i = lane; i < 16 * NA * 8; i += 32) (&stage.terms[0][0])[i] = 0u;
+    // lane r < rows follows row r's level and the ties it may still keep
+    const int my_level = lane < rows ? sh.level[lane] : -1;
+    int my_quota = lane < rows ? sh.quota[lane] : 0;
+
+    for (int seg = 0; seg < segs; ++seg) {
+        const int s0 = u0 + seg * cap, n = min(cap, u1 - s0);
+        const int wb = warp_begin(n, warp), we = warp_begin(n, warp + 1);
+        if (segs > 1) {                       // the slice did not fit: again from the bits
+            __syncthreads();
+            load_pages(s0, n);
+            __syncthreads();
+            distances(s0, wb, we, false);
         }
-        const bool keep = dist < t_level || (dist == t_level && before < t_quota);
-        t_quota -= min(all, t_quota);
-        const unsigned kept = __ballot_sync(kFullMask, keep);
-        if (lane == 0) warp_kept[warp] = __popc(kept);
-        __syncthreads();
-        int slot = __popc(kept & ((1u << lane) - 1)), n = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            slot += w < warp ? warp_kept[w] : 0;
-            n += warp_kept[w];
+        // ties of each row in this warp's part
+        for (int q = 0; q < RW; ++q) {
+            uint32_t same = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int l = __shfl_sync(kFullMask, my_level, 4 * q + i);
+                same |= (l < 0 ? 0xfeu : (uint32_t)l) << (8 * i);
+            }
+            uint32_t mine = 0;                // a byte per row: at most cap / 256 = 64 keys a lane
+            for (int k = wb + lane; k < we; k += 32)
+                mine += __vcmpeq4(distw[q * cap + k], same) & 0x01010101u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int s = __reduce_add_sync(kFullMask, mine >> (8 * i) & 255u);
+                if (lane == 0 && 4 * q + i < rows) sh.ties[warp][4 * q + i] = s;
+            }
         }
-        if (keep) {
-            kept_row[slot] = at;
-            kept_p[slot] = weight[dist];
-        }
         __syncthreads();
-        for (int k = part; k < n; k += kParts) {
-            const long long r = kept_row[k];
-            const uint32_t code = a.c.vcodes[r * (D / 2) + pair], sz = a.c.vscale[r];
-            acc0 = fmaf(kept_p[k], fmaf((float)(code & 15u), bf16_lo(sz), bf16_hi(sz)), acc0);
-            acc1 = fmaf(kept_p[k], fmaf((float)(code >> 4), bf16_lo(sz), bf16_hi(sz)), acc1);
+        int before = 0, all = 0, here = 0;
+        if (lane < rows) {
+            for (int w = 0; w < kCacheAttnWarps; ++w) {
+                const int x = sh.ties[w][lane];
+                before += w < warp ? x : 0;
+                all += x;
+                here = w == warp ? x : here;
+            }
+        }
+        // keep bytes below `limit`; a row whose quota ends inside this part
+        // keeps its first `left` ties
+        int left = my_quota - before;
+        const bool partial = left > 0 && left < here;
+        const int limit = my_level < 0 ? 0 : my_level + (left >= here);
+        my_quota = max(0, my_quota - all);
+        const unsigned partial_rows = __ballot_sync(kFullMask, partial);
+        uint32_t below[RWM];
+#pragma unroll
+        for (int q = 0; q < RWM; ++q) {
+            below[q] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                below[q] |= (uint32_t)__shfl_sync(kFullMask, limit, 4 * q + i) << (8 * i);
+        }
+        int listed = 0;
+        for (int k0 = wb; k0 < we; k0 += 32) {
+            const int k = k0 + lane;
+            uint32_t any = 0, d4[RWM];
+            const uint32_t at = k < we ? pool_row[k] : kNoRow;
+#pragma unroll
+            for (int q = 0; q < RWM; ++q) {
+                d4[q] = 0xffffffffu;
+                if (q >= RW) continue;
+                if (k < we) d4[q] = distw[q * cap + k];
+                uint32_t keep = __vcmpltu4(d4[q], below[q]);
+                for (unsigned todo = partial_rows >> (4 * q) & 15u; todo; todo &= todo - 1) {
+                    const int i = __ffs(todo) - 1, r = 4 * q + i;
+                    const int l = __shfl_sync(kFullMask, my_level, r);
+                    const int room = __shfl_sync(kFullMask, left, r);
+                    const bool tie = (int)(d4[q] >> (8 * i) & 255u) == l;
+                    const unsigned ties = __ballot_sync(kFullMask, tie);
+                    if (tie && __popc(ties & ((1u << lane) - 1)) < room) keep |= 255u << (8 * i);
+                    if (lane == r) left -= min(left, __popc(ties));
+                }
+                d4[q] |= ~keep;
+                any |= keep;
+            }
+            const unsigned kept = __ballot_sync(kFullMask, any != 0u);
+            __syncwarp();                     // all have read their keys
+            if (any) {
+                const int to = wb + listed + __popc(kept & ((1u << lane) - 1));
+                pool_row[to] = at;
+#pragma unroll
+                for (int q = 0; q < RWM; ++q)
+                    if (q < RW) distw[q * cap + to] = d4[q];
+            }
+            listed += __popc(kept);
+            __syncwarp();
+        }
+
+        // P V over the listed keys, 16 at a time, kStages - 1 chunks of
+        // copies ahead; a chunk that the list does not fill repeats its last
+        // key, which then weighs nothing
+        const int chunks = (listed + 15) / 16;
+        auto issue = [&](int c) {
+            if (c < chunks) {
+                constexpr int kPieces = D / 32;            // 16-byte pieces of a key's codes
+                const int ring = c % kStages, last = wb + listed - 1, k0 = wb + 16 * c;
+#pragma unroll
+                for (int i = lane; i < 16 * kPieces; i += 32) {
+                    const int k = i / kPieces, piece = i % kPieces;
+                    copy_async16(stage.codes[ring] + k * Stage::kStride + 16 * piece,
+                                 a.c.vcodes + (size_t)pool_row[min(k0 + k, last)] * (D / 2) + 16 * piece);
+                }
+                if (lane < 16)
+                    copy_async4(&stage.scale[ring][lane], a.c.vscale + pool_row[min(k0 + lane, last)]);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int c = 0; c < kStages - 1; ++c) issue(c);
+        for (int c = 0; c < chunks; ++c) {
+            issue(c + kStages - 1);
+            asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
+            __syncwarp();
+            const int ring = c % kStages;
+            {
+                // weights of keys 2 (lane % 8) and the next for every fourth row,
+                // as terms: the upper 8 bits of what is left, twice, and the rest
+                const int pair = lane & 7, k = 16 * c + 2 * pair;
+                const uint2 sz = *reinterpret_cast<const uint2 *>(&stage.scale[ring][2 * pair]);
+                const float s0f = bf16_lo(sz.x), z0 = fmaf(8.0f, s0f, bf16_hi(sz.x));
+                const float s1f = bf16_lo(sz.y), z1 = fmaf(8.0f, s1f, bf16_hi(sz.y));
+#pragma unroll
+                for (int i = 0; i < RWM; ++i) {
+                    const int r = 4 * i + (lane >> 3);
+                    if (r < rows) {
+                        // (two words from an even place: behind the list, within the warp's part)
+                        const uint2 d4 = *reinterpret_cast<const uint2 *>(distw + i * cap + wb + k);
+                        const uint32_t h0 = d4.x >> (8 * (lane >> 3)) & 255u;
+                        const uint32_t h1 = d4.y >> (8 * (lane >> 3)) & 255u;
+                        const bool keep0 = k < listed && h0 != kUnseen;
+                        const bool keep1 = k + 1 < listed && h1 != kUnseen;
+                        const float p0 = sh.p[r][min(h0, (uint32_t)D)], p1 = sh.p[r][min(h1, (uint32_t)D)];
+                        const float v0 = keep0 ? p0 * s0f : 0.0f, v1 = keep1 ? p1 * s1f : 0.0f;
+                        zacc[i] += keep0 ? p0 * z0 : 0.0f;
+                        zacc[i] += keep1 ? p1 * z1 : 0.0f;
+                        const float a0 = v0 - __uint_as_float(__float_as_uint(v0) & 0xffff0000u);
+                        const float a1 = v1 - __uint_as_float(__float_as_uint(v1) & 0xffff0000u);
+                        const float b0 = a0 - __uint_as_float(__float_as_uint(a0) & 0xffff0000u);
+                        const float b1 = a1 - __uint_as_float(__float_as_uint(a1) & 0xffff0000u);
+                        stage.terms[r][pair] = __byte_perm(__float_as_uint(v0), __float_as_uint(v1), 0x7632);
+                        stage.terms[R + r][pair] = __byte_perm(__float_as_uint(a0), __float_as_uint(a1), 0x7632);
+                        stage.terms[2 * R + r][pair] = __byte_perm(__float_as_uint(b0), __float_as_uint(b1), 0x7632);
+                    }
+                }
+            }
+            __syncwarp();
+            // this lane's four keys are 4 t4 .. 4 t4 + 3 and stand for columns
+            // 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of A; its codes of a key are
+            // elements g D/8 on
+            uint32_t af[NA][4], code[4][kCodeWords];
+#pragma unroll
+            for (int i = 0; i < 2 * NA; ++i) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(&stage.terms[g + 8 * i][2 * t4]);
+                af[i / 2][i % 2] = u.x;
+                af[i / 2][2 + i % 2] = u.y;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const unsigned char *from = stage.codes[ring] + (4 * t4 + e) * Stage::kStride + g * (D / 16);
+                if constexpr (kCodeWords == 1) {
+                    code[e][0] = *reinterpret_cast<const uint32_t *>(from);
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(from);
+                    code[e][0] = u.x; code[e][1] = u.y;
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < kCodeWords; ++w)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t sel = half ? 0x7632 : 0x5410;
+                    const uint32_t x0 = __byte_perm(code[0][w], code[1][w], sel);
+                    const uint32_t x1 = __byte_perm(code[2][w], code[3][w], sel);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t b0 = codes_bf16(x0 >> (4 * i)), b1 = codes_bf16(x1 >> (4 * i));
+#pragma unroll
+                        for (int m = 0; m < NA; ++m) mma_bf16(acc[m][8 * w + 4 * half + i], af[m], b0, b1);
+                    }
+                }
+            __syncwarp();
         }
     }
-    sums[part][2 * pair] = acc0;
-    sums[part][2 * pair + 1] = acc1;
+
+    // a row's p z: eight lanes hold its parts
+#pragma unroll
+    for (int i = 0; i < RWM; ++i)
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) zacc[i] += __shfl_xor_sync(kFullMask, zacc[i], o);
+    float *const red = reinterpret_cast<float *>(attn_smem);
+    constexpr int kRegs = cache_attn_red_regs<D, NA>(), kAcc = kRegs - RWM;
+#pragma unroll
+    for (int half = kCacheAttnWarps / 2; half > 0; half >>= 1) {
+        __syncthreads();
+        if (warp >= half && warp < 2 * half) {
+            float *to = red + (warp - half) * kRegs * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < kAcc; ++i) to[i * 32] = acc[i / (4 * kTiles)][i / 4 % kTiles][i % 4];
+#pragma unroll
+            for (int i = 0; i < RWM; ++i) to[(kAcc + i) * 32] = zacc[i];
+        }
+        __syncthreads();
+        if (warp < half) {
+            const float *from = red + warp * kRegs * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < kAcc; ++i) acc[i / (4 * kTiles)][i / 4 % kTiles][i % 4] += from[i * 32];
+#pragma unroll
+            for (int i = 0; i < RWM; ++i) zacc[i] += from[(kAcc + i) * 32];
+        }
+    }
     __syncthreads();
-    if (tid < D) {
-        float o = sums[0][tid];
-        for (int k = 1; k < kParts; ++k) o += sums[k][tid];
-        a.out[row * D + tid] = o;
+    if (warp == 0) {                          // stacked rows [16 NA][D]; column n of tile i: element n D/8 + i
+#pragma unroll
+        for (int m = 0; m < NA; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i)
+                    red[(16 * m + g + 8 * (e / 2)) * D + (2 * t4 + e % 2) * kTiles + i] = acc[m][i][e];
+#pragma unroll
+        for (int i = 0; i < RWM; ++i)
+            if ((lane & 7) == 0 && 4 * i + (lane >> 3) < rows) sh.zsum[4 * i + (lane >> 3)] = zacc[i];
+    }
+    __syncthreads();
+    for (int e = tid; e < rows * D; e += kCacheAttnThreads) {
+        const int r = e / D, k = e % D;
+        const float sum = red[(2 * R + r) * D + k] + red[(R + r) * D + k] + red[r * D + k] + sh.zsum[r];
+        if (C > 1) sh.part[r][k] = sum;
+        else a.out[q_row(r) * D + k] = sum;
+    }
+    if (C > 1) {
+        cluster.sync();
+        for (int e = rank * kCacheAttnThreads + tid; e < rows * D; e += C * kCacheAttnThreads) {
+            const int r = e / D, k = e % D;
+            float sum = 0.0f;
+            for (int o = 0; o < C; ++o) sum += *cluster.map_shared_rank(&sh.part[r][k], o);
+            a.out[q_row(r) * D + k] = sum;
+        }
+        cluster.sync();                       // the others have read this CTA's part
     }
 }
 
