@@ -68,17 +68,14 @@ def _declare(lib):
 
 
 _lib = _declare(_had._lib)
-_INT = torch.int32
+_INT, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_Tensor = torch.Tensor
 
 
 def _dev(t, name, dtype, ndim, device=None):
     """``t`` as a contiguous CUDA tensor of this type and number of dimensions."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    # a decode step makes these checks dozens of times: one test when all is well
-    if t.is_cuda and t.is_contiguous() and t.dim() == ndim and \
-            (dtype is None or t.dtype is dtype) and (device is None or t.device == device):
-        return t
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the HAD library has no CPU path)")
     if not t.is_contiguous():
@@ -87,26 +84,29 @@ def _dev(t, name, dtype, ndim, device=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
-    raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-
-
-def _ints(t, name, n, device):
-    """An int32 vector of n entries; its address."""
-    _dev(t, name, _INT, 1, device)
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
-    return t.data_ptr()
-
-
-def _opt(t, name, n, device):
-    return None if t is None else _ints(t, name, n, device)
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    return t
 
 
 def _shaped(t, name, dtype, shape, device):
-    _dev(t, name, dtype, len(shape), device)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return t
+    """The address of ``t``, a contiguous CUDA tensor of this type and shape."""
+    # a step of a decoder makes these checks dozens of times: one expression
+    # when all is well (0.4 us), the reasons otherwise
+    if not (isinstance(t, _Tensor) and t.shape == shape and t.dtype is dtype and
+            t.is_contiguous() and t.device == device and t.is_cuda):
+        _dev(t, name, dtype, len(shape), device)
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _ints(t, name, n, device):
+    """The address of an int32 vector of n entries."""
+    return _shaped(t, name, _INT, (n,), device)
+
+
+def _opt(t, name, n, device):
+    return None if t is None else _shaped(t, name, _INT, (n,), device)
 
 
 # Handles without the Python objects around them (2 us of a call each).
@@ -157,21 +157,17 @@ class Cache:
     [pages, heads, page, d/2] uint8, vscale [pages, heads, page, 2] bfloat16.
     Holds the tensors; a program keeps one per layer."""
 
+    __slots__ = ("kbits", "vcodes", "vscale", "pages", "heads", "page", "d", "device", "_pool")
+
     def __init__(self, kbits, vcodes, vscale):
-        _dev(kbits, "kbits", _INT, 4)
-        _dev(vcodes, "vcodes", torch.uint8, 4, kbits.device)
-        _dev(vscale, "vscale", torch.bfloat16, 4, kbits.device)
-        pages, heads, page, words = kbits.shape
-        if vcodes.shape != (pages, heads, page, 16 * words) or vscale.shape != (pages, heads, page, 2):
-            raise ValueError("kbits, vcodes and vscale must be [pages, heads, page, d/32], "
-                             f"[.., d/2] and [.., 2], got {tuple(kbits.shape)}, "
-                             f"{tuple(vcodes.shape)} and {tuple(vscale.shape)}")
-        self.kbits, self.vcodes, self.vscale = kbits, vcodes, vscale
+        pages, heads, page, words = _dev(kbits, "kbits", _INT, 4).shape
+        self.kbits, self.vcodes, self.vscale, self.device = kbits, vcodes, vscale, kbits.device
         self.pages, self.heads, self.page, self.d = pages, heads, page, 32 * words
-        self.device = kbits.device
-        self._pool = _Pool(kbits.data_ptr(), vcodes.data_ptr(), vscale.data_ptr(), pages, heads,
-                           page, self.d)
-        self._ref = ctypes.byref(self._pool)
+        self._pool = _Pool(kbits.data_ptr(),
+                           _shaped(vcodes, "vcodes", torch.uint8, (pages, heads, page, 16 * words),
+                                   self.device),
+                           _shaped(vscale, "vscale", _BF16, (pages, heads, page, 2), self.device),
+                           pages, heads, page, 32 * words)
 
     @classmethod
     def empty(cls, pages, heads, page, d, device="cuda"):
@@ -192,12 +188,14 @@ def empty_books(seqs, max_pages, pages, device="cuda"):
             torch.zeros(pages, dtype=_INT, device=device))
 
 
+_CODES = {_BF16: HAD_BF16, _F32: HAD_F32}
+
+
 def _dtype_code(t, name):
-    if t.dtype == torch.bfloat16:
-        return HAD_BF16
-    if t.dtype == torch.float32:
-        return HAD_F32
-    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return code
 
 
 def _of(cache):
@@ -206,23 +204,26 @@ def _of(cache):
     return cache
 
 
+def _table(table, B, dev):
+    """The address and the row length of the table of B sequences."""
+    width = table.shape[-1] if isinstance(table, _Tensor) and table.dim() == 2 else 0
+    return _shaped(table, "table", _INT, (B, width), dev), width
+
+
 def had_cache_append(k, v, sigma_k, cache, table, start, counts=None, dev_status=None,
                      stream=None):
     """Write tokens k, v [B, heads, T, d] of table rows [B, max_pages] from position start[b] on;
     of row b the first counts[b] (default: all T)."""
     dev = _of(cache).device
-    B, H, T, d = _dev(k, "k", None, 4, dev).shape
+    B, H, T, d = shape = _dev(k, "k", None, 4, dev).shape
     if H != cache.heads or d != cache.d:
-        raise ValueError(f"k must be [B, {cache.heads}, T, {cache.d}], got {tuple(k.shape)}")
-    _shaped(v, "v", k.dtype, (B, H, T, d), dev)
-    _shaped(sigma_k, "sigma_k", torch.float32, (H,), dev)
-    width = _rows(table, B, dev)
-    p_start, p_counts = _ints(start, "start", B, dev), _opt(counts, "counts", B, dev)
-    p_status = _opt(dev_status, "dev_status", 1, dev)
+        raise ValueError(f"k must be [B, {cache.heads}, T, {cache.d}], got {tuple(shape)}")
+    args = (k.data_ptr(), _shaped(v, "v", k.dtype, shape, dev), _dtype_code(k, "k"),
+            _shaped(sigma_k, "sigma_k", _F32, (H,), dev), cache._pool, *_table(table, B, dev),
+            _ints(start, "start", B, dev), _opt(counts, "counts", B, dev), B, T,
+            _opt(dev_status, "dev_status", 1, dev))
     with _on(dev, stream) as s:
-        _check(_lib.had_cache_append(k.data_ptr(), v.data_ptr(), _dtype_code(k, "k"),
-                                     sigma_k.data_ptr(), cache._ref, table.data_ptr(), width,
-                                     p_start, p_counts, B, T, p_status, s), "had_cache_append")
+        _check(_lib.had_cache_append(*args, s), "had_cache_append")
 
 
 def had_cache_read(cache, table, start, T, counts=None, bits=None, values=None, dev_status=None,
@@ -231,18 +232,17 @@ def had_cache_read(cache, table, start, T, counts=None, bits=None, values=None, 
     (bits [B, heads, T, d/32] int32, values [B, heads, T, d] float32), zeros behind the count."""
     dev = _of(cache).device
     B = _dev(table, "table", _INT, 2, dev).shape[0]
-    width = _rows(table, B, dev)
-    p_start, p_counts = _ints(start, "start", B, dev), _opt(counts, "counts", B, dev)
+    args = (cache._pool, *_table(table, B, dev), _ints(start, "start", B, dev),
+            _opt(counts, "counts", B, dev), B, _int(T, "T"))
     p_status = _opt(dev_status, "dev_status", 1, dev)
+    like_bits, like_values = (B, cache.heads, T, cache.d // 32), (B, cache.heads, T, cache.d)
     with _on(dev, stream) as s:
         if bits is None:
-            bits = torch.empty((B, cache.heads, T, cache.d // 32), dtype=_INT, device=dev)
+            bits = torch.empty(like_bits, dtype=_INT, device=dev)
         if values is None:
-            values = torch.empty((B, cache.heads, T, cache.d), dtype=torch.float32, device=dev)
-        _shaped(bits, "bits", _INT, (B, cache.heads, T, cache.d // 32), dev)
-        _shaped(values, "values", torch.float32, (B, cache.heads, T, cache.d), dev)
-        _check(_lib.had_cache_read(cache._ref, table.data_ptr(), width, p_start, p_counts, B, T,
-                                   bits.data_ptr(), values.data_ptr(), p_status, s),
+            values = torch.empty(like_values, dtype=_F32, device=dev)
+        _check(_lib.had_cache_read(*args, _shaped(bits, "bits", _INT, like_bits, dev),
+                                   _shaped(values, "values", _F32, like_values, dev), p_status, s),
                "had_cache_read")
     return bits, values
 
@@ -253,104 +253,88 @@ def had_cache_attention(q, sigma_q, cache, table, lens, N, tau, window=0, sinks=
     lens[b] cached ones: the N best visible keys, within `window` positions and the first
     `sinks` tokens if window > 0; returns out [B, Hq, T, d] float32."""
     dev = _of(cache).device
-    B, Hq, T, d = _dev(q, "q", None, 4, dev).shape
+    B, Hq, T, d = shape = _dev(q, "q", None, 4, dev).shape
     if d != cache.d:
-        raise ValueError(f"q must be [B, Hq, T, {cache.d}], got {tuple(q.shape)}")
-    _shaped(sigma_q, "sigma_q", torch.float32, (Hq,), dev)
-    width = _rows(table, B, dev)
-    p_lens, p_counts = _ints(lens, "lens", B, dev), _opt(counts, "counts", B, dev)
+        raise ValueError(f"q must be [B, Hq, T, {cache.d}], got {tuple(shape)}")
+    args = (q.data_ptr(), _dtype_code(q, "q"), _shaped(sigma_q, "sigma_q", _F32, (Hq,), dev),
+            cache._pool, *_table(table, B, dev), _ints(lens, "lens", B, dev),
+            _opt(counts, "counts", B, dev), B, Hq, T, _int(N, "N"), tau, _int(window, "window"),
+            _int(sinks, "sinks"))
     p_status = _opt(dev_status, "dev_status", 1, dev)
     with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty((B, Hq, T, d), dtype=torch.float32, device=dev)
-        else:
-            _shaped(out, "out", torch.float32, (B, Hq, T, d), dev)
-        _check(_lib.had_cache_attention(q.data_ptr(), _dtype_code(q, "q"), sigma_q.data_ptr(),
-                                        cache._ref, table.data_ptr(), width, p_lens, p_counts, B,
-                                        Hq, T, _int(N, "N"), tau, _int(window, "window"),
-                                        _int(sinks, "sinks"), out.data_ptr(), p_status, s),
+            out = torch.empty_like(q, dtype=_F32)
+        _check(_lib.had_cache_attention(*args, _shaped(out, "out", _F32, shape, dev), p_status, s),
                "had_cache_attention")
     return out
 
 
-def _rows(table, B, dev):
-    """Entries of a row of the table of B sequences."""
-    _dev(table, "table", _INT, 2, dev)
-    if table.shape[0] != B:
-        raise ValueError(f"table must have {B} rows, got {table.shape[0]}")
-    return table.shape[1]
-
-
 def _books(table, lens, refs):
-    """Device, S, max_pages and pages of the books of a call."""
-    dev = _dev(table, "table", _INT, 2).device
-    S, width = table.shape
-    if lens is not None:
-        _ints(lens, "lens", S, dev)
-    _dev(refs, "refs", _INT, 1, dev)
-    return dev, S, width, refs.numel()
+    """Device of a call on the books, and (table, lens, refs, S, max_pages, pages); without
+    lens where a call has none."""
+    S, width = _dev(table, "table", _INT, 2).shape
+    dev = table.device
+    P = _dev(refs, "refs", _INT, 1, dev).shape[0]
+    if lens is None:
+        return dev, (table.data_ptr(), refs.data_ptr(), S, width, P)
+    return dev, (table.data_ptr(), _ints(lens, "lens", S, dev), refs.data_ptr(), S, width, P)
 
 
 def had_cache_fork(table, lens, refs, page, src, dst, dev_status=None, stream=None):
     """Sequence dst[i] continues as a copy of sequence src[i], for all i at once; in place."""
-    dev, S, width, P = _books(table, lens, refs)
-    n = _dev(src, "src", _INT, 1, dev).numel()
-    p_dst = _ints(dst, "dst", n, dev)
-    p_status = _opt(dev_status, "dev_status", 1, dev)
+    dev, books = _books(table, lens, refs)
+    n = _dev(src, "src", _INT, 1, dev).shape[0]
+    args = (*books, _int(page, "page"), src.data_ptr(), _ints(dst, "dst", n, dev), n,
+            _opt(dev_status, "dev_status", 1, dev))
     with _on(dev, stream) as s:
-        _check(_lib.had_cache_fork(table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, width,
-                                   P, _int(page, "page"), src.data_ptr(), p_dst, n, p_status, s),
-               "had_cache_fork")
+        _check(_lib.had_cache_fork(*args, s), "had_cache_fork")
 
 
 def had_cache_reserve(table, lens, refs, page, grow, src=None, dst=None, dev_status=None,
                       stream=None):
     """Room for grow[s] more tokens of every sequence, in place; returns (src [S], dst [S]) int32,
     the shared last pages to be copied (-1: none) with had_cache_copy_pages."""
-    dev, S, width, P = _books(table, lens, refs)
-    p_grow = _ints(grow, "grow", S, dev)
+    dev, books = _books(table, lens, refs)
+    S = lens.shape[0]
+    args = (*books, _int(page, "page"), _ints(grow, "grow", S, dev))
     p_status = _opt(dev_status, "dev_status", 1, dev)
     with _on(dev, stream) as s:
-        src = torch.empty(S, dtype=_INT, device=dev) if src is None else src
-        dst = torch.empty(S, dtype=_INT, device=dev) if dst is None else dst
-        _check(_lib.had_cache_reserve(table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S,
-                                      width, P, _int(page, "page"), p_grow, _ints(src, "src", S, dev),
-                                      _ints(dst, "dst", S, dev), p_status, s),
-               "had_cache_reserve")
+        src = torch.empty_like(lens) if src is None else src
+        dst = torch.empty_like(lens) if dst is None else dst
+        _check(_lib.had_cache_reserve(*args, _ints(src, "src", S, dev), _ints(dst, "dst", S, dev),
+                                      p_status, s), "had_cache_reserve")
     return src, dst
 
 
 def had_cache_free(table, lens, refs, seqs, dev_status=None, stream=None):
     """The sequences listed in seqs [n] let their pages go and become empty; in place."""
-    dev, S, width, P = _books(table, lens, refs)
-    n = _dev(seqs, "seqs", _INT, 1, dev).numel()
-    p_status = _opt(dev_status, "dev_status", 1, dev)
+    dev, books = _books(table, lens, refs)
+    n = _dev(seqs, "seqs", _INT, 1, dev).shape[0]
+    args = (*books, seqs.data_ptr(), n, _opt(dev_status, "dev_status", 1, dev))
     with _on(dev, stream) as s:
-        _check(_lib.had_cache_free(table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, width,
-                                   P, seqs.data_ptr(), n, p_status, s), "had_cache_free")
+        _check(_lib.had_cache_free(*args, s), "had_cache_free")
 
 
 def had_cache_evict(table, lens, refs, page, window, sinks=0, dev_status=None, stream=None):
     """Every sequence lets go of the pages that lie wholly in [sinks, lens - window); in place."""
-    dev, S, width, P = _books(table, lens, refs)
-    p_status = _opt(dev_status, "dev_status", 1, dev)
+    dev, books = _books(table, lens, refs)
+    args = (*books, _int(page, "page"), _int(window, "window"), _int(sinks, "sinks"),
+            _opt(dev_status, "dev_status", 1, dev))
     with _on(dev, stream) as s:
-        _check(_lib.had_cache_evict(table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, width,
-                                    P, _int(page, "page"), _int(window, "window"),
-                                    _int(sinks, "sinks"), p_status, s), "had_cache_evict")
+        _check(_lib.had_cache_evict(*args, s), "had_cache_evict")
 
 
 def had_cache_compact(table, refs, src=None, dst=None, live=None, dev_status=None, stream=None):
     """Renames the used pages to 0 .. live - 1, in place; returns (src [pages], dst [pages],
     live [1]) int32, the pages to be copied (-1: none) with had_cache_copy_pages."""
-    dev, S, width, P = _books(table, None, refs)
+    dev, books = _books(table, None, refs)
+    P = refs.shape[0]
     p_status = _opt(dev_status, "dev_status", 1, dev)
     with _on(dev, stream) as s:
-        src = torch.empty(P, dtype=_INT, device=dev) if src is None else src
-        dst = torch.empty(P, dtype=_INT, device=dev) if dst is None else dst
+        src = torch.empty_like(refs) if src is None else src
+        dst = torch.empty_like(refs) if dst is None else dst
         live = torch.empty(1, dtype=_INT, device=dev) if live is None else live
-        _check(_lib.had_cache_compact(table.data_ptr(), refs.data_ptr(), S, width, P,
-                                      _ints(src, "src", P, dev), _ints(dst, "dst", P, dev),
+        _check(_lib.had_cache_compact(*books, _ints(src, "src", P, dev), _ints(dst, "dst", P, dev),
                                       _ints(live, "live", 1, dev), p_status, s),
                "had_cache_compact")
     return src, dst, live
@@ -359,9 +343,8 @@ def had_cache_compact(table, refs, src=None, dst=None, live=None, dev_status=Non
 def had_cache_copy_pages(cache, src, dst, dev_status=None, stream=None):
     """Copies page src[i] to page dst[i] of the pool; pairs with a negative index are skipped."""
     dev = _of(cache).device
-    n = _dev(src, "src", _INT, 1, dev).numel()
-    p_dst = _ints(dst, "dst", n, dev)
-    p_status = _opt(dev_status, "dev_status", 1, dev)
+    n = _dev(src, "src", _INT, 1, dev).shape[0]
+    args = (cache._pool, src.data_ptr(), _ints(dst, "dst", n, dev), n,
+            _opt(dev_status, "dev_status", 1, dev))
     with _on(dev, stream) as s:
-        _check(_lib.had_cache_copy_pages(cache._ref, src.data_ptr(), p_dst, n, p_status, s),
-               "had_cache_copy_pages")
+        _check(_lib.had_cache_copy_pages(*args, s), "had_cache_copy_pages")

@@ -121,7 +121,7 @@ class HostCache(cache.Cache):
     def __init__(self):
         self.pages, self.heads, self.page, self.d = 8, 2, 16, 64
         self.device = torch.device("cpu")
-        self._ref = pool()
+        self._pool = cache._Pool(FAKE, FAKE, FAKE, 8, 2, 16, 64)
 
 
 HOST = HostCache()
