@@ -121,16 +121,17 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, had::Cach
         const long long seen = (long long)a.window + a.sinks + plan.R;
         keys = seen < keys ? seen : keys;
     }
-    // 48 KB of rows and distances at once, so that two CTAs share an SM
-    const long long most = 48 * 1024 / had::cache_attn_key_bytes(plan.R) / 256 * 256;
-    // CTAs until two per SM are busy, each with 256 keys or more, and until a
+    // 20 KB of distances at once, so that four CTAs share an SM
+    const long long most = 20 * 1024 / had::cache_attn_key_bytes(plan.R) / 128 * 128;
+    // CTAs until four per SM are busy, each with 256 keys or more, and until a
     // CTA holds its slice whole (a longer one is gone through twice)
     const long long tiles = (long long)B * a.c.heads * plan.tiles;
     plan.ctas = 1;
-    while (plan.ctas < 8 && (keys + 32 * plan.ctas > most * plan.ctas ||
-                             (tiles * plan.ctas * 2 <= 2 * 148 && keys > 256LL * plan.ctas)))
+    while (plan.ctas < had::kMaxCtas &&
+           (keys > most * plan.ctas ||
+            (tiles * plan.ctas * 2 <= 4 * 148 && keys > 256LL * plan.ctas)))
         plan.ctas *= 2;
-    const long long per = ((keys + plan.ctas - 1) / plan.ctas + 32 + 255) / 256 * 256;
+    const long long per = (keys + 128 * plan.ctas - 1) / (128 * plan.ctas) * 128;
     plan.cap = (int)(per < most ? per : most);
     if (tiles * plan.ctas > INT_MAX) return HAD_ERR_UNSUPPORTED;
     return launch_clusters(had::cache_attn_kernel<T, D, NA>, (unsigned)(tiles * plan.ctas),

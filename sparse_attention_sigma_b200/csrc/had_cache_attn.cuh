@@ -13,16 +13,17 @@
 //
 // One cluster of CTAs takes a tile of R rows that share a key-value head (its
 // query heads, and neighbouring tokens of a draft or chunk) and splits the keys
-// that any of them sees; a CTA's eight warps split its slice, in key order.
+// that any of them sees; a CTA's four warps split its slice, in key order.
 //   1. Distances: a lane per key, the key's bits in registers, XOR + popc with
 //      every row's bits from shared memory; 8-bit distances stay in shared
 //      memory (255: not visible), counts go to the CTA's histograms.
 //   2. The cluster's histograms are read through distributed shared memory; a
 //      warp per row finds level, quota and Z and fills p[h].  The ties that
 //      lower-ranked CTAs hold come from the same counts.
-//   3. Each warp drops what its rows do not keep (ties by rank in key order)
-//      and moves the keys that at least one row keeps to the front of its part.
-//   4. Per 16 listed keys: the tile's P V on the tensor core.  The codes are
+//   3. Each warp goes through its part again, drops what a row does not keep
+//      (ties by rank in key order) and queues the keys that at least one row
+//      keeps; their codes and scales are copied to shared memory from there.
+//   4. Per 16 queued keys, three chunks behind the copies: the tile's P V on the tensor core.  The codes are
 //      whole numbers below 16, exact in bf16; the weights p s are fp32 and are
 //      cut into three bf16 terms, which hold all 24 bits, and stacked as rows
 //      of A: row x = term R + r.  So the product is as exact as fp32 and any
@@ -64,15 +65,16 @@ __device__ __forceinline__ RowRange row_range(const CacheAttnArgs &a, int len, i
     return r;
 }
 
-constexpr int kCacheAttnThreads = 256;
+constexpr int kCacheAttnThreads = 128;
 constexpr int kCacheAttnWarps = kCacheAttnThreads / 32;
+constexpr int kMaxCtas = 8;            // of a cluster
 constexpr uint32_t kUnseen = 255u;     // distance byte of a key that a row does not keep
 
 // Rows of a tile: three terms each in NA tiles of 16 stacked rows.
 __host__ __device__ constexpr int cache_attn_rows(int na) { return na * 16 / 3; }
 
 // The tile's split: R rows, `tiles` tiles per (sequence, head), `ctas` per
-// cluster, `cap` keys a CTA holds at once (a multiple of 256).
+// cluster, `cap` keys a CTA holds at once (a multiple of 128).
 struct CacheAttnPlan {
     int R, tiles, ctas, cap;
 };
@@ -81,10 +83,13 @@ struct CacheAttnPlan {
 // tokens and the window) that need not begin with a page.
 __host__ __device__ constexpr int cache_attn_pages(int cap) { return cap / 16 + 4; }
 
-// A warp's own shared memory in step 4: a ring of kStages chunks of 16 keys
-// (codes, rows padded by 16 bytes so that the eight lanes of a key and the four
-// keys of a load fall on different banks; scales), and the stacked rows of A.
+// A warp's own shared memory in steps 3 and 4: the queue of kept keys (row of
+// the pool, a distance per row of the tile), a ring of kStages chunks of 16
+// keys (codes, rows padded by 16 bytes so that the eight lanes of a key and the
+// four keys of a load fall on different banks; scales), and the stacked rows
+// of A.
 constexpr int kStages = 4;
+constexpr int kQueue = 128;            // >= 16 kStages + 15 + 32
 
 template <int D, int NA>
 struct WarpStage {
@@ -92,16 +97,25 @@ struct WarpStage {
     __align__(16) unsigned char codes[kStages][16 * kStride];
     __align__(8) uint32_t scale[kStages][16];
     __align__(16) uint32_t terms[16 * NA][8];        // bf16 of two neighbouring keys
+    uint32_t pool_row[kQueue];
+    __align__(8) uint32_t dist[(cache_attn_rows(NA) + 3) / 4][kQueue];
 };
 
-// Bytes of shared memory of a key: its row in the pool, a distance per row.
-__host__ __device__ constexpr int cache_attn_key_bytes(int R) { return 4 + (R + 3) / 4 * 4; }
+// Bytes of shared memory of a key of the slice: a distance per row.
+__host__ __device__ constexpr int cache_attn_key_bytes(int R) { return (R + 3) / 4 * 4; }
 
-// Floats of the cross-warp sums: accumulators and p z of one warp, per lane.
-template <int D, int NA>
-constexpr int cache_attn_red_regs()
+// The warps' results before they are added: [warps][16 NA][kSumStride] floats.
+// Column n of accumulator tile i is element n D/8 + i; its 16-byte piece i / 4
+// lies at place (i / 4) ^ sum_swizzle(n), and a row is padded, so that the
+// eight lanes of a store's wavefront (two rows, four columns) fall on different
+// banks.
+template <int D>
+constexpr int kSumStride = D + D / 8;
+
+template <int D>
+__device__ __forceinline__ int sum_swizzle(int n)
 {
-    return NA * D / 2 + (cache_attn_rows(NA) + 3) / 4;
+    return D == 128 ? n >> 1 : n >> 2;
 }
 
 template <int D, int NA>
@@ -109,7 +123,7 @@ size_t cache_attn_smem_bytes(const CacheAttnPlan &p)
 {
     const size_t keys = sizeof(WarpStage<D, NA>) * kCacheAttnWarps +
                         (size_t)p.cap * cache_attn_key_bytes(p.R) + cache_attn_pages(p.cap) * 4;
-    const size_t red = kCacheAttnWarps / 2 * 32 * 4 * cache_attn_red_regs<D, NA>();
+    const size_t red = sizeof(float) * kCacheAttnWarps * 16 * NA * kSumStride<D>;
     return keys > red ? keys : red;
 }
 
@@ -153,15 +167,18 @@ struct CacheAttnShared {
     __align__(16) uint32_t qbits[RM][D / 32];
     int pos[RM], lo[RM];
     int hist[RM][D + 1];
-    float p[RM][D + 1];
+    union {
+        float p[RM][D + 1];            // weight of a distance
+        float part[RM][D];             // at the end: this CTA's sums
+    };
     int level[RM], quota[RM];
+    int ranked;                        // some row keeps only part of its ties
     int ties[kCacheAttnWarps][RM];
-    float zsum[RM];
-    float part[RM][D];
+    float zsum[kCacheAttnWarps][RM];
 };
 
 template <typename T, int D, int NA>
-__global__ void __launch_bounds__(kCacheAttnThreads, NA * D <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(kCacheAttnThreads, NA * D <= 128 ? 4 : 2)
 cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 {
     constexpr int DW = D / 32;
@@ -179,8 +196,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     Stage &stage = reinterpret_cast<Stage *>(attn_smem)[warp];
     uint32_t *const distw = reinterpret_cast<uint32_t *>(                    // [RW][cap]
         attn_smem + sizeof(Stage) * kCacheAttnWarps);
-    uint32_t *const pool_row = distw + RW * cap;                             // [cap]
-    int *const page_of = reinterpret_cast<int *>(pool_row + cap);
+    int *const page_of = reinterpret_cast<int *>(distw + RW * cap);
 
     const int C = plan.ctas;
     const int rank = (int)(blockIdx.x % (unsigned)C);
@@ -193,34 +209,47 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     const int lg = a.c.page_log, page_mask = (1 << lg) - 1;
     const int32_t *const table = a.table + (long long)b * a.max_pages;
 
-    int len = __ldg(a.lens + b), count = a.counts ? __ldg(a.counts + b) : a.T;
-    if (len < 0 || len > (long long)a.max_pages << lg || count < 0 || count > a.T) {
-        if (tid == 0) flag(a.status, HAD_ERR_INVALID_ARG);
-        len = count = 0;
-    }
-
     // row r of the tile: token (row0 + r) / G, query head h G + (row0 + r) % G
     auto q_row = [&](int r) -> long long {
         const int t = (row0 + r) / G, g = (row0 + r) % G;
         return ((long long)b * a.Hq + h * G + g) * a.T + t;
     };
-    for (int r = warp; r < rows; r += kCacheAttnWarps) {
-        const long long at = q_row(r) * D;
-        const SignRule rule = sign_rule(__ldg(a.sigma + h * G + (row0 + r) % G));
-        if (rule.bad && lane == 0) flag(a.status, HAD_ERR_BAD_SIGMA);
+    int len = __ldg(a.lens + b), count = a.counts ? __ldg(a.counts + b) : a.T;
+    {
+        constexpr int kMine = (cache_attn_rows(NA) + kCacheAttnWarps - 1) / kCacheAttnWarps;
+        float x[kMine][DW], sigma[kMine];
 #pragma unroll
-        for (int w = 0; w < DW; ++w) {
-            const float x = (float)static_cast<const T *>(a.Q)[at + 32 * w + lane];
-            const uint32_t word = __ballot_sync(kFullMask, negative_bit(x, rule));
-            if (lane == 0) sh.qbits[r][w] = word;
+        for (int i = 0; i < kMine; ++i) {
+            const int r = min(warp + i * kCacheAttnWarps, rows - 1);
+            const T *from = static_cast<const T *>(a.Q) + q_row(r) * D + lane;
+            sigma[i] = __ldg(a.sigma + h * G + (row0 + r) % G);
+#pragma unroll
+            for (int w = 0; w < DW; ++w) x[i][w] = (float)from[32 * w];
         }
-        if (lane == 0) {
-            const RowRange rr = row_range(a, len, count, (row0 + r) / G);
-            sh.pos[r] = rr.pos;
-            sh.lo[r] = rr.lo;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int r = warp + i * kCacheAttnWarps;
+            if (r >= rows) break;
+            const SignRule rule = sign_rule(sigma[i]);
+            if (rule.bad && lane == 0) flag(a.status, HAD_ERR_BAD_SIGMA);
+#pragma unroll
+            for (int w = 0; w < DW; ++w) {
+                const uint32_t word = __ballot_sync(kFullMask, negative_bit(x[i][w], rule));
+                if (lane == 0) sh.qbits[r][w] = word;
+            }
         }
+        if (tid == 0) sh.ranked = 0;
     }
     for (int i = tid; i < R * (D + 1); i += kCacheAttnThreads) (&sh.hist[0][0])[i] = 0;
+    if (len < 0 || len > (long long)a.max_pages << lg || count < 0 || count > a.T) {
+        if (tid == 0) flag(a.status, HAD_ERR_INVALID_ARG);
+        len = count = 0;
+    }
+    if (tid < rows) {
+        const RowRange rr = row_range(a, len, count, (row0 + tid) / G);
+        sh.pos[tid] = rr.pos;
+        sh.lo[tid] = rr.lo;
+    }
 
     // keys that some row of the tile sees: [0, first_n) and [lo, hi]
     const int t_lo = max(row0 / G, count - len), t_hi = min((row0 + rows - 1) / G, count - 1);
@@ -244,6 +273,10 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     auto page_at = [&](int u) {               // index of u's page among the pages of all keys
         return u < first_n ? u >> lg : ((u - first_n + lo) >> lg) - (lo >> lg) + first_pages;
     };
+    auto pool_row_of = [&](int u, int page) -> uint32_t {
+        return ((page * (unsigned)a.c.heads + h) << lg) + (key_of(u) & page_mask);
+    };
+
     // Keys s0 .. s0 + n - 1 of the slice: their pages, then this warp's distances.
     auto load_pages = [&](int s0, int n) {
         if (n <= 0) return;
@@ -267,8 +300,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                 const int k = k0 + 32 * i + lane, u = min(s0 + k, s0 + we - 1);
                 const int page = page_of[page_at(u) - page0];
                 const bool have = k < we && page >= 0;
-                next_row[i] = have ? (uint32_t)(((page * (unsigned)a.c.heads + h) << lg) +
-                                                (key_of(u) & page_mask)) : kNoRow;
+                next_row[i] = have ? pool_row_of(u, page) : kNoRow;
 #pragma unroll
                 for (int w = 0; w < DW; ++w) next[i][w] = 0u;
                 if (have) {
@@ -330,7 +362,6 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 #pragma unroll
             for (int i = 0; i < KU; ++i) {
                 at[i] = next_row[i];
-                if (k0 + 32 * i + lane < we) pool_row[k0 + 32 * i + lane] = at[i];
 #pragma unroll
                 for (int w = 0; w < DW; ++w) bits[i][w] = next[i][w];
             }
@@ -343,7 +374,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         }
     };
     // a warp's part of n keys: whole groups of 32, in key order
-    auto warp_begin = [&](int n, int w) { return min(n, w * (((n + 255) / 256) * 32)); };
+    auto warp_begin = [&](int n, int w) { return min(n, w * (((n + kCacheAttnThreads - 1) / kCacheAttnThreads) * 32)); };
 
     for (int seg = 0; seg < segs; ++seg) {
         const int s0 = u0 + seg * cap, n = min(cap, u1 - s0);
@@ -362,7 +393,10 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         int cnt[EL], before[EL], sum = 0;
 #pragma unroll
         for (int e = 0; e < EL; ++e) cnt[e] = before[e] = 0;
-        for (int o = 0; o < C; ++o) {
+        // all of the cluster's counts in flight at once
+#pragma unroll
+        for (int o = 0; o < kMaxCtas; ++o) {
+            if (o >= C) break;
             const int *hist = C > 1 ? cluster.map_shared_rank(&sh.hist[r][0], o) : &sh.hist[r][0];
 #pragma unroll
             for (int e = 0; e < EL; ++e) {
@@ -389,6 +423,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                 level = lane * EL + e;
                 quota = n - cum;
                 sh.quota[r] = max(0, quota - before[e]);
+                if (quota < cnt[e]) sh.ranked = 1;
             }
             cum += cnt[e];
         }
@@ -405,9 +440,10 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFullMask, z, o);
+        const float inv = z > 0.0f ? __frcp_rn(z) : 0.0f;
 #pragma unroll
         for (int e = 0; e < EL; ++e)
-            if (lane * EL + e <= D) sh.p[r][lane * EL + e] = z > 0.0f ? w[e] / z : 0.0f;
+            if (lane * EL + e <= D) sh.p[r][lane * EL + e] = w[e] * inv;
         if (lane == 0) {
             sh.level[r] = level;
             if (level < 0) sh.quota[r] = 0;
@@ -440,7 +476,9 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
             __syncthreads();
             distances(s0, wb, we, false);
         }
-        // ties of each row in this warp's part
+        // ties of each row in this warp's part, where a row keeps only some
+        int before = 0, all = 0, here = 0;
+        if (sh.ranked) {
         for (int q = 0; q < RW; ++q) {
             uint32_t same = 0;
 #pragma unroll
@@ -448,7 +486,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                 const int l = __shfl_sync(kFullMask, my_level, 4 * q + i);
                 same |= (l < 0 ? 0xfeu : (uint32_t)l) << (8 * i);
             }
-            uint32_t mine = 0;                // a byte per row: at most cap / 256 = 64 keys a lane
+            uint32_t mine = 0;                // a byte per row: at most cap / 128 keys a lane
             for (int k = wb + lane; k < we; k += 32)
                 mine += __vcmpeq4(distw[q * cap + k], same) & 0x01010101u;
 #pragma unroll
@@ -458,7 +496,6 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
             }
         }
         __syncthreads();
-        int before = 0, all = 0, here = 0;
         if (lane < rows) {
             for (int w = 0; w < kCacheAttnWarps; ++w) {
                 const int x = sh.ties[w][lane];
@@ -467,11 +504,12 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                 here = w == warp ? x : here;
             }
         }
+        }
         // keep bytes below `limit`; a row whose quota ends inside this part
         // keeps its first `left` ties
         int left = my_quota - before;
         const bool partial = left > 0 && left < here;
-        const int limit = my_level < 0 ? 0 : my_level + (left >= here);
+        const int limit = my_level < 0 ? 0 : my_level + (left >= here);   // (unranked: all ties)
         my_quota = max(0, my_quota - all);
         const unsigned partial_rows = __ballot_sync(kFullMask, partial);
         uint32_t below[RWM];
@@ -482,11 +520,12 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
             for (int i = 0; i < 4; ++i)
                 below[q] |= (uint32_t)__shfl_sync(kFullMask, limit, 4 * q + i) << (8 * i);
         }
-        int listed = 0;
-        for (int k0 = wb; k0 < we; k0 += 32) {
+        const int page0 = n > 0 ? page_at(s0) : 0;
+        int queued = 0, k0 = wb;
+        // the next 32 keys of the part
+        auto look = [&]() {
             const int k = k0 + lane;
             uint32_t any = 0, d4[RWM];
-            const uint32_t at = k < we ? pool_row[k] : kNoRow;
 #pragma unroll
             for (int q = 0; q < RWM; ++q) {
                 d4[q] = 0xffffffffu;
@@ -506,41 +545,42 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                 any |= keep;
             }
             const unsigned kept = __ballot_sync(kFullMask, any != 0u);
-            __syncwarp();                     // all have read their keys
             if (any) {
-                const int to = wb + listed + __popc(kept & ((1u << lane) - 1));
-                pool_row[to] = at;
+                const int to = (queued + __popc(kept & ((1u << lane) - 1))) % kQueue, u = s0 + k;
+                stage.pool_row[to] = pool_row_of(u, page_of[page_at(u) - page0]);
 #pragma unroll
                 for (int q = 0; q < RWM; ++q)
-                    if (q < RW) distw[q * cap + to] = d4[q];
+                    if (q < RW) stage.dist[q][to] = d4[q];
             }
-            listed += __popc(kept);
-            __syncwarp();
-        }
-
-        // P V over the listed keys, 16 at a time, kStages - 1 chunks of
-        // copies ahead; a chunk that the list does not fill repeats its last
-        // key, which then weighs nothing
-        const int chunks = (listed + 15) / 16;
+            queued += __popc(kept);
+            k0 += 32;
+        };
+        // copies of the c-th 16 queued keys; one that the queue does not fill
+        // repeats its last key, which then weighs nothing
         auto issue = [&](int c) {
-            if (c < chunks) {
+            if (16 * c < queued) {
                 constexpr int kPieces = D / 32;            // 16-byte pieces of a key's codes
-                const int ring = c % kStages, last = wb + listed - 1, k0 = wb + 16 * c;
+                const int ring = c % kStages, last = queued - 1;
 #pragma unroll
                 for (int i = lane; i < 16 * kPieces; i += 32) {
                     const int k = i / kPieces, piece = i % kPieces;
+                    const uint32_t at = stage.pool_row[min(16 * c + k, last) % kQueue];
                     copy_async16(stage.codes[ring] + k * Stage::kStride + 16 * piece,
-                                 a.c.vcodes + (size_t)pool_row[min(k0 + k, last)] * (D / 2) + 16 * piece);
+                                 a.c.vcodes + (size_t)at * (D / 2) + 16 * piece);
                 }
                 if (lane < 16)
-                    copy_async4(&stage.scale[ring][lane], a.c.vscale + pool_row[min(k0 + lane, last)]);
+                    copy_async4(&stage.scale[ring][lane],
+                                a.c.vscale + stage.pool_row[min(16 * c + lane, last) % kQueue]);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-#pragma unroll
-        for (int c = 0; c < kStages - 1; ++c) issue(c);
-        for (int c = 0; c < chunks; ++c) {
-            issue(c + kStages - 1);
+        for (int ahead = 0;; ++ahead) {
+            while (queued < 16 * (ahead + 1) && k0 < we) look();
+            __syncwarp();
+            issue(ahead);
+            const int c = ahead - (kStages - 1);
+            if (c < 0) continue;
+            if (16 * c >= queued) break;                   // (all keys were looked at by then)
             asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
             __syncwarp();
             const int ring = c % kStages;
@@ -555,12 +595,11 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                 for (int i = 0; i < RWM; ++i) {
                     const int r = 4 * i + (lane >> 3);
                     if (r < rows) {
-                        // (two words from an even place: behind the list, within the warp's part)
-                        const uint2 d4 = *reinterpret_cast<const uint2 *>(distw + i * cap + wb + k);
+                        const uint2 d4 = *reinterpret_cast<const uint2 *>(&stage.dist[i][k % kQueue]);
                         const uint32_t h0 = d4.x >> (8 * (lane >> 3)) & 255u;
                         const uint32_t h1 = d4.y >> (8 * (lane >> 3)) & 255u;
-                        const bool keep0 = k < listed && h0 != kUnseen;
-                        const bool keep1 = k + 1 < listed && h1 != kUnseen;
+                        const bool keep0 = k < queued && h0 != kUnseen;
+                        const bool keep1 = k + 1 < queued && h1 != kUnseen;
                         const float p0 = sh.p[r][min(h0, (uint32_t)D)], p1 = sh.p[r][min(h1, (uint32_t)D)];
                         const float v0 = keep0 ? p0 * s0f : 0.0f, v1 = keep1 ? p1 * s1f : 0.0f;
                         zacc[i] += keep0 ? p0 * z0 : 0.0f;
@@ -619,44 +658,32 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     for (int i = 0; i < RWM; ++i)
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) zacc[i] += __shfl_xor_sync(kFullMask, zacc[i], o);
-    float *const red = reinterpret_cast<float *>(attn_smem);
-    constexpr int kRegs = cache_attn_red_regs<D, NA>(), kAcc = kRegs - RWM;
-#pragma unroll
-    for (int half = kCacheAttnWarps / 2; half > 0; half >>= 1) {
-        __syncthreads();
-        if (warp >= half && warp < 2 * half) {
-            float *to = red + (warp - half) * kRegs * 32 + lane;
-#pragma unroll
-            for (int i = 0; i < kAcc; ++i) to[i * 32] = acc[i / (4 * kTiles)][i / 4 % kTiles][i % 4];
-#pragma unroll
-            for (int i = 0; i < RWM; ++i) to[(kAcc + i) * 32] = zacc[i];
-        }
-        __syncthreads();
-        if (warp < half) {
-            const float *from = red + warp * kRegs * 32 + lane;
-#pragma unroll
-            for (int i = 0; i < kAcc; ++i) acc[i / (4 * kTiles)][i / 4 % kTiles][i % 4] += from[i * 32];
-#pragma unroll
-            for (int i = 0; i < RWM; ++i) zacc[i] += from[(kAcc + i) * 32];
-        }
-    }
+    constexpr int kStride = kSumStride<D>;
+    float *const sums = reinterpret_cast<float *>(attn_smem);
     __syncthreads();
-    if (warp == 0) {                          // stacked rows [16 NA][D]; column n of tile i: element n D/8 + i
 #pragma unroll
-        for (int m = 0; m < NA; ++m)
+    for (int m = 0; m < NA; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4; ++e) {
+            const int x = 16 * m + g + 8 * (e / 2), n = 2 * t4 + e % 2;
+            if (x >= 3 * R) continue;
+            float *to = sums + (warp * 16 * NA + x) * kStride + n * kTiles;
 #pragma unroll
-                for (int i = 0; i < kTiles; ++i)
-                    red[(16 * m + g + 8 * (e / 2)) * D + (2 * t4 + e % 2) * kTiles + i] = acc[m][i][e];
+            for (int i = 0; i < kTiles; i += 4)
+                *reinterpret_cast<float4 *>(to + ((i / 4) ^ sum_swizzle<D>(n)) * 4) =
+                    make_float4(acc[m][i][e], acc[m][i + 1][e], acc[m][i + 2][e], acc[m][i + 3][e]);
+        }
 #pragma unroll
-        for (int i = 0; i < RWM; ++i)
-            if ((lane & 7) == 0 && 4 * i + (lane >> 3) < rows) sh.zsum[4 * i + (lane >> 3)] = zacc[i];
-    }
+    for (int i = 0; i < RWM; ++i)
+        if ((lane & 7) == 0 && 4 * i + (lane >> 3) < rows) sh.zsum[warp][4 * i + (lane >> 3)] = zacc[i];
     __syncthreads();
     for (int e = tid; e < rows * D; e += kCacheAttnThreads) {
-        const int r = e / D, k = e % D;
-        const float sum = red[(2 * R + r) * D + k] + red[(R + r) * D + k] + red[r * D + k] + sh.zsum[r];
+        const int r = e / D, k = e % D, n = k / kTiles, i = k % kTiles;
+        const float *from = sums + r * kStride + n * kTiles + ((i / 4) ^ sum_swizzle<D>(n)) * 4 + i % 4;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kCacheAttnWarps; ++w, from += 16 * NA * kStride)
+            sum += (from[2 * R * kStride] + from[R * kStride] + sh.zsum[w][r]) + from[0];
         if (C > 1) sh.part[r][k] = sum;
         else a.out[q_row(r) * D + k] = sum;
     }
