@@ -123,17 +123,20 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, had::Cach
     }
     // 20 KB of distances at once, so that four CTAs share an SM
     const long long most = 20 * 1024 / had::cache_attn_key_bytes(plan.R) / 128 * 128;
-    // CTAs until four per SM are busy, each with 256 keys or more, and until a
+    // CTAs until four per SM are busy, each with 512 keys or more, and until a
     // CTA holds its slice whole (a longer one is gone through twice)
     const long long tiles = (long long)B * a.c.heads * plan.tiles;
     plan.ctas = 1;
     while (plan.ctas < had::kMaxCtas &&
            (keys > most * plan.ctas ||
-            (tiles * plan.ctas * 2 <= 4 * 148 && keys > 256LL * plan.ctas)))
+            (tiles * plan.ctas * 2 <= 4 * 148 && keys > 512LL * plan.ctas)))
         plan.ctas *= 2;
     const long long per = (keys + 128 * plan.ctas - 1) / (128 * plan.ctas) * 128;
     plan.cap = (int)(per < most ? per : most);
     if (tiles * plan.ctas > INT_MAX) return HAD_ERR_UNSUPPORTED;
+    plan.by_tiles = had::divisor((unsigned)plan.tiles);
+    plan.by_heads = had::divisor((unsigned)a.c.heads);
+    plan.by_group = had::divisor((unsigned)(a.Hq / a.c.heads));
     return launch_clusters(had::cache_attn_kernel<T, D, NA>, (unsigned)(tiles * plan.ctas),
                            (unsigned)plan.ctas, had::kCacheAttnThreads,
                            had::cache_attn_smem_bytes<D, NA>(plan), st, a, plan);

@@ -16,14 +16,14 @@
 // that any of them sees; a CTA's four warps split its slice, in key order.
 //   1. Distances: a lane per key, the key's bits in registers, XOR + popc with
 //      every row's bits from shared memory; 8-bit distances stay in shared
-//      memory (255: not visible), counts go to the CTA's histograms.
+//      memory (d + 1: not visible), counts go to the CTA's histograms.
 //   2. The cluster's histograms are read through distributed shared memory; a
 //      warp per row finds level, quota and Z and fills p[h].  The ties that
 //      lower-ranked CTAs hold come from the same counts.
 //   3. Each warp goes through its part again, drops what a row does not keep
 //      (ties by rank in key order) and queues the keys that at least one row
 //      keeps; their codes and scales are copied to shared memory from there.
-//   4. Per 16 queued keys, three chunks behind the copies: the tile's P V on the tensor core.  The codes are
+//   4. Per 16 queued keys, behind their copies: the tile's P V on the tensor core.  The codes are
 //      whole numbers below 16, exact in bf16; the weights p s are fp32 and are
 //      cut into three bf16 terms, which hold all 24 bits, and stacked as rows
 //      of A: row x = term R + r.  So the product is as exact as fp32 and any
@@ -68,7 +68,6 @@ __device__ __forceinline__ RowRange row_range(const CacheAttnArgs &a, int len, i
 constexpr int kCacheAttnThreads = 128;
 constexpr int kCacheAttnWarps = kCacheAttnThreads / 32;
 constexpr int kMaxCtas = 8;            // of a cluster
-constexpr uint32_t kUnseen = 255u;     // distance byte of a key that a row does not keep
 
 // Rows of a tile: three terms each in NA tiles of 16 stacked rows.
 __host__ __device__ constexpr int cache_attn_rows(int na) { return na * 16 / 3; }
@@ -77,6 +76,7 @@ __host__ __device__ constexpr int cache_attn_rows(int na) { return na * 16 / 3; 
 // cluster, `cap` keys a CTA holds at once (a multiple of 128).
 struct CacheAttnPlan {
     int R, tiles, ctas, cap;
+    Divisor by_tiles, by_heads, by_group;      // of tiles, heads, query heads per head
 };
 
 // Entries of the list of pages under `cap` keys: two runs of keys (the first
@@ -89,14 +89,14 @@ __host__ __device__ constexpr int cache_attn_pages(int cap) { return cap / 16 + 
 // four keys of a load fall on different banks; scales), and the stacked rows
 // of A.
 constexpr int kStages = 4;
-constexpr int kQueue = 128;            // >= 16 kStages + 15 + 32
+constexpr int kQueue = 128;            // >= 16 (kStages + 1) + 31
 
 template <int D, int NA>
 struct WarpStage {
     static constexpr int kStride = D / 2 + 16;
     __align__(16) unsigned char codes[kStages][16 * kStride];
     __align__(8) uint32_t scale[kStages][16];
-    __align__(16) uint32_t terms[16 * NA][8];        // bf16 of two neighbouring keys
+    __align__(16) uint32_t terms[2][16 * NA][8];     // bf16 of two neighbouring keys
     uint32_t pool_row[kQueue];
     __align__(8) uint32_t dist[(cache_attn_rows(NA) + 3) / 4][kQueue];
 };
@@ -139,6 +139,16 @@ __device__ __forceinline__ void copy_async4(void *to, const void *from)
                  :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
 }
 
+// A word of another CTA's shared memory, by its address in one's own.
+__device__ __forceinline__ int load_of_cta(uint32_t at, int cta)
+{
+    uint32_t there;
+    int x;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(cta));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(there) : "memory");
+    return x;
+}
+
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
@@ -161,14 +171,24 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t x)
     return r;
 }
 
+// 255 in the bytes where a < b (unsigned), 0 in the others
+__device__ __forceinline__ uint32_t bytes_below(uint32_t a, uint32_t b)
+{
+    const uint32_t t = (a | 0x80808080u) - (b & 0x7f7f7f7fu);      // bit 7 clear: low 7 bits of a less
+    const uint32_t less = (~a & b) | (~(a ^ b) & ~t);              // in bit 7
+    uint32_t spread;                                               // bit 7 over the byte
+    asm("prmt.b32 %0, %1, %2, 0xba98;" : "=r"(spread) : "r"(less), "r"(0u));
+    return spread;
+}
+
 template <int D, int NA>
 struct CacheAttnShared {
     static constexpr int RM = cache_attn_rows(NA);
     __align__(16) uint32_t qbits[RM][D / 32];
     int pos[RM], lo[RM];
-    int hist[RM][D + 1];
+    int hist[RM][D + 2];               // a distance of D + 1: not seen
     union {
-        float p[RM][D + 1];            // weight of a distance
+        float p[RM][D + 2];            // weight of a distance; 0 for D + 1
         float part[RM][D];             // at the end: this CTA's sums
     };
     int level[RM], quota[RM];
@@ -178,14 +198,14 @@ struct CacheAttnShared {
 };
 
 template <typename T, int D, int NA>
-__global__ void __launch_bounds__(kCacheAttnThreads, NA * D <= 128 ? 4 : 2)
+__global__ void __launch_bounds__(kCacheAttnThreads, NA * D <= 64 ? 5 : NA * D <= 128 ? 4 : 2)
 cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 {
     constexpr int DW = D / 32;
     constexpr int kTiles = D / 8;             // 8-wide column tiles of the value
     constexpr int kCodeWords = D / 64;        // 32-bit words of codes per lane and key
     constexpr int RWM = (cache_attn_rows(NA) + 3) / 4;        // most words of four row bytes
-    constexpr uint32_t kNoRow = 0xffffffffu;
+    constexpr uint32_t kNoRow = 0xffffffffu, kUnseen = D + 1, kUnseen4 = kUnseen * 0x01010101u;
     constexpr int KU = 4;                     // keys per lane of one step of the distances
     using Shared = CacheAttnShared<D, NA>;
     extern __shared__ __align__(16) unsigned char attn_smem[];
@@ -196,22 +216,22 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     Stage &stage = reinterpret_cast<Stage *>(attn_smem)[warp];
     uint32_t *const distw = reinterpret_cast<uint32_t *>(                    // [RW][cap]
         attn_smem + sizeof(Stage) * kCacheAttnWarps);
-    int *const page_of = reinterpret_cast<int *>(distw + RW * cap);
+    uint32_t *const page_row = distw + RW * cap;                             // first row of a page
 
     const int C = plan.ctas;
-    const int rank = (int)(blockIdx.x % (unsigned)C);
-    const unsigned unit = blockIdx.x / (unsigned)C;
-    const int tile = (int)(unit % (unsigned)plan.tiles);
-    const unsigned bh = unit / (unsigned)plan.tiles;
-    const int h = (int)(bh % (unsigned)a.c.heads), b = (int)(bh / (unsigned)a.c.heads);
-    const int G = a.Hq / a.c.heads;
+    const int rank = (int)(blockIdx.x & (unsigned)(C - 1));        // C is a power of two
+    const unsigned unit = blockIdx.x >> (__ffs(C) - 1);
+    const unsigned bh = divide(unit, plan.by_tiles), b = divide(bh, plan.by_heads);
+    const int tile = (int)(unit - bh * (unsigned)plan.tiles);
+    const int h = (int)(bh - b * (unsigned)a.c.heads), G = (int)plan.by_group.d;
     const int row0 = tile * R, rows = min(R, G * a.T - row0);
     const int lg = a.c.page_log, page_mask = (1 << lg) - 1;
     const int32_t *const table = a.table + (long long)b * a.max_pages;
 
     // row r of the tile: token (row0 + r) / G, query head h G + (row0 + r) % G
+    auto token_of = [&](int r) { return (int)divide((unsigned)(row0 + r), plan.by_group); };
     auto q_row = [&](int r) -> long long {
-        const int t = (row0 + r) / G, g = (row0 + r) % G;
+        const int t = token_of(r), g = row0 + r - t * G;
         return ((long long)b * a.Hq + h * G + g) * a.T + t;
     };
     int len = __ldg(a.lens + b), count = a.counts ? __ldg(a.counts + b) : a.T;
@@ -222,7 +242,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         for (int i = 0; i < kMine; ++i) {
             const int r = min(warp + i * kCacheAttnWarps, rows - 1);
             const T *from = static_cast<const T *>(a.Q) + q_row(r) * D + lane;
-            sigma[i] = __ldg(a.sigma + h * G + (row0 + r) % G);
+            sigma[i] = __ldg(a.sigma + h * G + row0 + r - token_of(r) * G);
 #pragma unroll
             for (int w = 0; w < DW; ++w) x[i][w] = (float)from[32 * w];
         }
@@ -240,19 +260,20 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         }
         if (tid == 0) sh.ranked = 0;
     }
-    for (int i = tid; i < R * (D + 1); i += kCacheAttnThreads) (&sh.hist[0][0])[i] = 0;
+    for (int i = tid; i < R * (D + 2); i += kCacheAttnThreads) (&sh.hist[0][0])[i] = 0;
     if (len < 0 || len > (long long)a.max_pages << lg || count < 0 || count > a.T) {
         if (tid == 0) flag(a.status, HAD_ERR_INVALID_ARG);
         len = count = 0;
     }
     if (tid < rows) {
-        const RowRange rr = row_range(a, len, count, (row0 + tid) / G);
+        const RowRange rr = row_range(a, len, count, token_of(tid));
         sh.pos[tid] = rr.pos;
         sh.lo[tid] = rr.lo;
     }
 
     // keys that some row of the tile sees: [0, first_n) and [lo, hi]
-    const int t_lo = max(row0 / G, count - len), t_hi = min((row0 + rows - 1) / G, count - 1);
+    const int t_first = token_of(0), t_last = token_of(rows - 1);
+    const int t_lo = max(t_first, count - len), t_hi = min(t_last, count - 1);
     int lo = 0, first_n = 0, total = 0;
     int min_pos = -1, max_lo = 0;             // a key in [max_lo, min_pos] is seen by every row
     if (t_lo <= t_hi) {
@@ -261,7 +282,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         first_n = from.sinks;
         total = first_n + to.pos + 1 - lo;
         max_lo = to.lo;
-        if (row0 / G == t_lo && (row0 + rows - 1) / G == t_hi) min_pos = from.pos;
+        if (t_first == t_lo && t_last == t_hi) min_pos = from.pos;
     }
     const int first_pages = (first_n + page_mask) >> lg;
     // this CTA's slice of them, whole groups of 32
@@ -269,25 +290,20 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     const int u0 = min(total, rank * per), u1 = min(total, u0 + per);
     const int segs = max(1, (u1 - u0 + cap - 1) / cap);
 
-    auto key_of = [&](int u) { return u < first_n ? u : u - first_n + lo; };
-    auto page_at = [&](int u) {               // index of u's page among the pages of all keys
-        return u < first_n ? u >> lg : ((u - first_n + lo) >> lg) - (lo >> lg) + first_pages;
-    };
-    auto pool_row_of = [&](int u, int page) -> uint32_t {
-        return ((page * (unsigned)a.c.heads + h) << lg) + (key_of(u) & page_mask);
-    };
+    // key u of them: its position; its page's index among the pages of all of them
+    const int to_key = lo - first_n, to_page = first_pages - (lo >> lg);
+    auto key_of = [&](int u) { return u < first_n ? u : u + to_key; };
+    auto page_at = [&](int u) { return (key_of(u) >> lg) + (u < first_n ? 0 : to_page); };
 
     // Keys s0 .. s0 + n - 1 of the slice: their pages, then this warp's distances.
     auto load_pages = [&](int s0, int n) {
         if (n <= 0) return;
         const int first = page_at(s0), last = page_at(s0 + n - 1);
         for (int i = first + tid; i <= last; i += kCacheAttnThreads) {
-            int page = __ldg(table + (i < first_pages ? i : i - first_pages + (lo >> lg)));
-            if (page < 0 || page >= a.c.pages) {
-                flag(a.status, HAD_ERR_INVALID_ARG);
-                page = -1;
-            }
-            page_of[i - first] = page;
+            const int page = __ldg(table + (i < first_pages ? i : i - to_page));
+            const bool there = page >= 0 && page < a.c.pages;
+            if (!there) flag(a.status, HAD_ERR_INVALID_ARG);
+            page_row[i - first] = there ? (page * (unsigned)a.c.heads + h) << lg : kNoRow;
         }
     };
     auto distances = [&](int s0, int wb, int we, bool with_hist) {
@@ -297,10 +313,10 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         auto fetch = [&](int k0) {
 #pragma unroll
             for (int i = 0; i < KU; ++i) {
-                const int k = k0 + 32 * i + lane, u = min(s0 + k, s0 + we - 1);
-                const int page = page_of[page_at(u) - page0];
-                const bool have = k < we && page >= 0;
-                next_row[i] = have ? pool_row_of(u, page) : kNoRow;
+                const int u = min(s0 + k0 + 32 * i + lane, s0 + we - 1);
+                const uint32_t first = page_row[page_at(u) - page0];
+                const bool have = k0 + 32 * i + lane < we && first != kNoRow;
+                next_row[i] = have ? first + (key_of(u) & page_mask) : kNoRow;
 #pragma unroll
                 for (int w = 0; w < DW; ++w) next[i][w] = 0u;
                 if (have) {
@@ -319,11 +335,15 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
             for (int q = 0; q < RW; ++q) {
                 uint32_t word[KU];
 #pragma unroll
-                for (int i = 0; i < KU; ++i) word[i] = 0xffffffffu;
+                for (int i = 0; i < KU; ++i) word[i] = 0u;
 #pragma unroll
                 for (int rr = 0; rr < 4; ++rr) {
                     const int r = 4 * q + rr;
-                    if (r >= rows) break;
+                    if (r >= rows) {
+#pragma unroll
+                        for (int i = 0; i < KU; ++i) word[i] += kUnseen << (8 * rr);
+                        continue;
+                    }
                     uint32_t qb[DW];
                     if constexpr (DW == 2) {
                         const uint2 x = *reinterpret_cast<const uint2 *>(sh.qbits[r]);
@@ -335,6 +355,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                     const int pos = mixed ? sh.pos[r] : 0, row_lo = mixed ? sh.lo[r] : 0;
 #pragma unroll
                     for (int i = 0; i < KU; ++i) {
+                        if (k0 + 32 * i >= we) break;
                         int n = 0;
 #pragma unroll
                         for (int w = 0; w < DW; ++w) n += __popc(bits[i][w] ^ qb[w]);
@@ -343,10 +364,9 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                             const int key = key_of(s0 + k0 + 32 * i + lane);
                             vis = vis && key <= pos && (key >= row_lo || key < a.sinks);
                         }
-                        if (vis) {
-                            word[i] ^= (kUnseen ^ (uint32_t)n) << (8 * rr);
-                            if (with_hist) atomicAdd(&sh.hist[r][n], 1);
-                        }
+                        n = vis ? n : (int)kUnseen;
+                        word[i] += (uint32_t)n << (8 * rr);
+                        if (with_hist) atomicAdd(&sh.hist[r][n], 1);
                     }
                 }
 #pragma unroll
@@ -389,22 +409,49 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 
     // level, quota and weights: a warp per row, EL consecutive levels per lane
     for (int r = warp; r < rows; r += kCacheAttnWarps) {
-        constexpr int EL = (D + 1 + 31) / 32;
+        constexpr int EL = (D + 2 + 31) / 32;
         int cnt[EL], before[EL], sum = 0;
 #pragma unroll
         for (int e = 0; e < EL; ++e) cnt[e] = before[e] = 0;
-        // all of the cluster's counts in flight at once
+        if (C > 1) {
+            // the cluster's counts, neighbouring words by neighbouring lanes and
+            // four CTAs' in flight at once, through this warp's shared memory
+            // to the order in which they are added up
+            int all[EL], below[EL];
 #pragma unroll
-        for (int o = 0; o < kMaxCtas; ++o) {
-            if (o >= C) break;
-            const int *hist = C > 1 ? cluster.map_shared_rank(&sh.hist[r][0], o) : &sh.hist[r][0];
+            for (int e = 0; e < EL; ++e) all[e] = below[e] = 0;
+            const uint32_t here = (uint32_t)__cvta_generic_to_shared(&sh.hist[r][lane]);
+            for (int o0 = 0; o0 < C; o0 += 4) {
+                int x[4][EL];
+#pragma unroll
+                for (int o = 0; o < 4; ++o)
+#pragma unroll
+                    for (int e = 0; e < EL; ++e)
+                        x[o][e] = o0 + o < C && lane + 32 * e <= D ? load_of_cta(here + 128 * e, o0 + o) : 0;
+#pragma unroll
+                for (int o = 0; o < 4; ++o)
+#pragma unroll
+                    for (int e = 0; e < EL; ++e) {
+                        all[e] += x[o][e];
+                        below[e] += o0 + o < rank ? x[o][e] : 0;
+                    }
+            }
+            int *const to = reinterpret_cast<int *>(stage.codes);
 #pragma unroll
             for (int e = 0; e < EL; ++e) {
-                const int l = lane * EL + e;
-                const int x = l <= D ? hist[l] : 0;
-                cnt[e] += x;
-                before[e] += o < rank ? x : 0;
+                to[lane + 32 * e] = all[e];
+                to[32 * EL + lane + 32 * e] = below[e];
             }
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < EL; ++e) {
+                cnt[e] = to[lane * EL + e];
+                before[e] = to[32 * EL + lane * EL + e];
+            }
+            __syncwarp();
+        } else {
+#pragma unroll
+            for (int e = 0; e < EL; ++e) cnt[e] = lane * EL + e <= D ? sh.hist[r][lane * EL + e] : 0;
         }
 #pragma unroll
         for (int e = 0; e < EL; ++e) sum += cnt[e];
@@ -431,11 +478,14 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         const int owner = __reduce_max_sync(kFullMask, level >= 0 ? lane : -1);
         level = __shfl_sync(kFullMask, level, max(owner, 0));
         quota = __shfl_sync(kFullMask, quota, max(owner, 0));
+        // exp(tau (s_l - s_first)) = 2^(2 tau log2(e) (first - l)); a tau so large
+        // that the product overflows leaves the first level alone, as it should
+        const float rate = fminf(2.8853901f * a.tau, FLT_MAX);
         float w[EL], z = 0.0f;
 #pragma unroll
         for (int e = 0; e < EL; ++e) {
             const int l = lane * EL + e;
-            w[e] = l <= level && cnt[e] > 0 ? expf(a.tau * (float)(2 * (first - l))) : 0.0f;
+            w[e] = l <= level && cnt[e] > 0 ? exp2f(rate * (float)(first - l)) : 0.0f;
             z += w[e] * (float)(l < level ? cnt[e] : quota);
         }
 #pragma unroll
@@ -443,7 +493,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         const float inv = z > 0.0f ? __frcp_rn(z) : 0.0f;
 #pragma unroll
         for (int e = 0; e < EL; ++e)
-            if (lane * EL + e <= D) sh.p[r][lane * EL + e] = w[e] * inv;
+            if (lane * EL + e <= D + 1) sh.p[r][lane * EL + e] = lane * EL + e <= D ? w[e] * inv : 0.0f;
         if (lane == 0) {
             sh.level[r] = level;
             if (level < 0) sh.quota[r] = 0;
@@ -462,7 +512,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 #pragma unroll
     for (int i = 0; i < RWM; ++i) zacc[i] = 0.0f;
     // stacked rows that no term fills stay zero
-    for (int i = lane; i < 16 * NA * 8; i += 32) (&stage.terms[0][0])[i] = 0u;
+    for (int i = lane; i < 2 * 16 * NA * 8; i += 32) (&stage.terms[0][0][0])[i] = 0u;
     // lane r < rows follows row r's level and the ties it may still keep
     const int my_level = lane < rows ? sh.level[lane] : -1;
     int my_quota = lane < rows ? sh.quota[lane] : 0;
@@ -484,7 +534,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int l = __shfl_sync(kFullMask, my_level, 4 * q + i);
-                same |= (l < 0 ? 0xfeu : (uint32_t)l) << (8 * i);
+                same |= (l < 0 ? 0xffu : (uint32_t)l) << (8 * i);
             }
             uint32_t mine = 0;                // a byte per row: at most cap / 128 keys a lane
             for (int k = wb + lane; k < we; k += 32)
@@ -528,10 +578,10 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
             uint32_t any = 0, d4[RWM];
 #pragma unroll
             for (int q = 0; q < RWM; ++q) {
-                d4[q] = 0xffffffffu;
+                d4[q] = kUnseen4;
                 if (q >= RW) continue;
                 if (k < we) d4[q] = distw[q * cap + k];
-                uint32_t keep = __vcmpltu4(d4[q], below[q]);
+                uint32_t keep = bytes_below(d4[q], below[q]);
                 for (unsigned todo = partial_rows >> (4 * q) & 15u; todo; todo &= todo - 1) {
                     const int i = __ffs(todo) - 1, r = 4 * q + i;
                     const int l = __shfl_sync(kFullMask, my_level, r);
@@ -541,87 +591,104 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                     if (tie && __popc(ties & ((1u << lane) - 1)) < room) keep |= 255u << (8 * i);
                     if (lane == r) left -= min(left, __popc(ties));
                 }
-                d4[q] |= ~keep;
+                d4[q] = (d4[q] & keep) | (kUnseen4 & ~keep);
                 any |= keep;
             }
             const unsigned kept = __ballot_sync(kFullMask, any != 0u);
             if (any) {
                 const int to = (queued + __popc(kept & ((1u << lane) - 1))) % kQueue, u = s0 + k;
-                stage.pool_row[to] = pool_row_of(u, page_of[page_at(u) - page0]);
+                stage.pool_row[to] = page_row[page_at(u) - page0] + (key_of(u) & page_mask);
 #pragma unroll
                 for (int q = 0; q < RWM; ++q)
                     if (q < RW) stage.dist[q][to] = d4[q];
             }
             queued += __popc(kept);
             k0 += 32;
+            if (k0 >= we && queued > 0) {
+                // the last chunk repeats its last key, which then weighs nothing
+                __syncwarp();
+                const int to = queued + lane;
+                if (lane < (-queued & 15)) {
+                    stage.pool_row[to % kQueue] = stage.pool_row[(queued - 1) % kQueue];
+#pragma unroll
+                    for (int q = 0; q < RWM; ++q)
+                        if (q < RW) stage.dist[q][to % kQueue] = kUnseen4;
+                }
+            }
         };
-        // copies of the c-th 16 queued keys; one that the queue does not fill
-        // repeats its last key, which then weighs nothing
+        // copies of the c-th 16 queued keys: 16-byte pieces of their codes, and scales
+        constexpr int kPieces = D / 32;
         auto issue = [&](int c) {
             if (16 * c < queued) {
-                constexpr int kPieces = D / 32;            // 16-byte pieces of a key's codes
-                const int ring = c % kStages, last = queued - 1;
+                const int ring = c % kStages;
+                const uint32_t *const from = stage.pool_row + 16 * c % kQueue;
+                unsigned char *const to = stage.codes[ring] + lane / kPieces * Stage::kStride + lane % kPieces * 16;
 #pragma unroll
-                for (int i = lane; i < 16 * kPieces; i += 32) {
-                    const int k = i / kPieces, piece = i % kPieces;
-                    const uint32_t at = stage.pool_row[min(16 * c + k, last) % kQueue];
-                    copy_async16(stage.codes[ring] + k * Stage::kStride + 16 * piece,
-                                 a.c.vcodes + (size_t)at * (D / 2) + 16 * piece);
-                }
-                if (lane < 16)
-                    copy_async4(&stage.scale[ring][lane],
-                                a.c.vscale + stage.pool_row[min(16 * c + lane, last) % kQueue]);
+                for (int i = 0; i < 16 * kPieces / 32; ++i)
+                    copy_async16(to + i * (32 / kPieces) * Stage::kStride,
+                                 a.c.vcodes + (size_t)from[i * (32 / kPieces) + lane / kPieces] * (D / 2) +
+                                     lane % kPieces * 16);
+                if (lane < 16) copy_async4(&stage.scale[ring][lane], a.c.vscale + from[lane]);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        for (int ahead = 0;; ++ahead) {
-            while (queued < 16 * (ahead + 1) && k0 < we) look();
-            __syncwarp();
-            issue(ahead);
-            const int c = ahead - (kStages - 1);
-            if (c < 0) continue;
-            if (16 * c >= queued) break;                   // (all keys were looked at by then)
-            asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
-            __syncwarp();
+        // weights of chunk c: keys 2 (lane % 8) and the next for every fourth row,
+        // as terms: the upper 8 bits of what is left, twice, and the rest
+        auto weigh = [&](int c) {
             const int ring = c % kStages;
-            {
-                // weights of keys 2 (lane % 8) and the next for every fourth row,
-                // as terms: the upper 8 bits of what is left, twice, and the rest
-                const int pair = lane & 7, k = 16 * c + 2 * pair;
-                const uint2 sz = *reinterpret_cast<const uint2 *>(&stage.scale[ring][2 * pair]);
-                const float s0f = bf16_lo(sz.x), z0 = fmaf(8.0f, s0f, bf16_hi(sz.x));
-                const float s1f = bf16_lo(sz.y), z1 = fmaf(8.0f, s1f, bf16_hi(sz.y));
+            uint32_t (*const terms)[8] = stage.terms[c & 1];
+            const int pair = lane & 7, sub = lane >> 3;
+            const uint2 sz = *reinterpret_cast<const uint2 *>(&stage.scale[ring][2 * pair]);
+            const float s_a = bf16_lo(sz.x), z_a = fmaf(8.0f, s_a, bf16_hi(sz.x));
+            const float s_b = bf16_lo(sz.y), z_b = fmaf(8.0f, s_b, bf16_hi(sz.y));
+            // a NaN scale must not meet the weight 0 of a row that drops the key
+            const bool odd = __any_sync(kFullMask, s_a != s_a || s_b != s_b);
 #pragma unroll
-                for (int i = 0; i < RWM; ++i) {
-                    const int r = 4 * i + (lane >> 3);
-                    if (r < rows) {
-                        const uint2 d4 = *reinterpret_cast<const uint2 *>(&stage.dist[i][k % kQueue]);
-                        const uint32_t h0 = d4.x >> (8 * (lane >> 3)) & 255u;
-                        const uint32_t h1 = d4.y >> (8 * (lane >> 3)) & 255u;
-                        const bool keep0 = k < queued && h0 != kUnseen;
-                        const bool keep1 = k + 1 < queued && h1 != kUnseen;
-                        const float p0 = sh.p[r][min(h0, (uint32_t)D)], p1 = sh.p[r][min(h1, (uint32_t)D)];
-                        const float v0 = keep0 ? p0 * s0f : 0.0f, v1 = keep1 ? p1 * s1f : 0.0f;
-                        zacc[i] += keep0 ? p0 * z0 : 0.0f;
-                        zacc[i] += keep1 ? p1 * z1 : 0.0f;
-                        const float a0 = v0 - __uint_as_float(__float_as_uint(v0) & 0xffff0000u);
-                        const float a1 = v1 - __uint_as_float(__float_as_uint(v1) & 0xffff0000u);
-                        const float b0 = a0 - __uint_as_float(__float_as_uint(a0) & 0xffff0000u);
-                        const float b1 = a1 - __uint_as_float(__float_as_uint(a1) & 0xffff0000u);
-                        stage.terms[r][pair] = __byte_perm(__float_as_uint(v0), __float_as_uint(v1), 0x7632);
-                        stage.terms[R + r][pair] = __byte_perm(__float_as_uint(a0), __float_as_uint(a1), 0x7632);
-                        stage.terms[2 * R + r][pair] = __byte_perm(__float_as_uint(b0), __float_as_uint(b1), 0x7632);
+            for (int i = 0; i < RWM; ++i) {
+                const int r = 4 * i + sub;
+                if (r < rows) {
+                    const uint2 d4 = *reinterpret_cast<const uint2 *>(&stage.dist[i][(16 * c + 2 * pair) % kQueue]);
+                    const uint32_t h_a = __byte_perm(d4.x, 0u, 0x4440 | sub), h_b = __byte_perm(d4.y, 0u, 0x4440 | sub);
+                    const float p_a = sh.p[r][h_a], p_b = sh.p[r][h_b];
+                    float v_a = p_a * s_a, v_b = p_b * s_b, z = fmaf(p_a, z_a, p_b * z_b);
+                    if (odd) {
+                        v_a = h_a == kUnseen ? 0.0f : v_a;
+                        v_b = h_b == kUnseen ? 0.0f : v_b;
+                        z = (h_a == kUnseen ? 0.0f : p_a * z_a) + (h_b == kUnseen ? 0.0f : p_b * z_b);
                     }
+                    zacc[i] += z;
+                    const float m_a = v_a - __uint_as_float(__float_as_uint(v_a) & 0xffff0000u);
+                    const float m_b = v_b - __uint_as_float(__float_as_uint(v_b) & 0xffff0000u);
+                    const float l_a = m_a - __uint_as_float(__float_as_uint(m_a) & 0xffff0000u);
+                    const float l_b = m_b - __uint_as_float(__float_as_uint(m_b) & 0xffff0000u);
+                    terms[r][pair] = __byte_perm(__float_as_uint(v_a), __float_as_uint(v_b), 0x7632);
+                    terms[R + r][pair] = __byte_perm(__float_as_uint(m_a), __float_as_uint(m_b), 0x7632);
+                    terms[2 * R + r][pair] = __byte_perm(__float_as_uint(l_a), __float_as_uint(l_b), 0x7632);
                 }
             }
+        };
+        // Step i issues the copies of chunk i, weighs chunk i - 2 and multiplies
+        // chunk i - 3: the two are independent, and one warp barrier stands
+        // between a step's writes and the next step's reads.
+        for (int step_i = 0;; ++step_i) {
+            while (queued < 16 * (step_i + 1) && k0 < we) look();
+            const int c = step_i - 3;
+            if (c >= 0 && 16 * c >= queued) break;         // (all keys were looked at by then)
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncwarp();
+            issue(step_i);
+            if (c < 0) {
+                if (c == -1 && queued > 0) weigh(0);
+                continue;
+            }
+            const int ring = c % kStages;
             // this lane's four keys are 4 t4 .. 4 t4 + 3 and stand for columns
             // 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of A; its codes of a key are
             // elements g D/8 on
             uint32_t af[NA][4], code[4][kCodeWords];
 #pragma unroll
             for (int i = 0; i < 2 * NA; ++i) {
-                const uint2 u = *reinterpret_cast<const uint2 *>(&stage.terms[g + 8 * i][2 * t4]);
+                const uint2 u = *reinterpret_cast<const uint2 *>(&stage.terms[c & 1][g + 8 * i][2 * t4]);
                 af[i / 2][i % 2] = u.x;
                 af[i / 2][2 + i % 2] = u.y;
             }
@@ -635,6 +702,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                     code[e][0] = u.x; code[e][1] = u.y;
                 }
             }
+            if (16 * (c + 1) < queued) weigh(c + 1);
 #pragma unroll
             for (int w = 0; w < kCodeWords; ++w)
 #pragma unroll
@@ -649,8 +717,8 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                         for (int m = 0; m < NA; ++m) mma_bf16(acc[m][8 * w + 4 * half + i], af[m], b0, b1);
                     }
                 }
-            __syncwarp();
         }
+        __syncwarp();
     }
 
     // a row's p z: eight lanes hold its parts
