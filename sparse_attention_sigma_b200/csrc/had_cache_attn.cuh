@@ -69,8 +69,9 @@ constexpr int kCacheAttnThreads = 128;
 constexpr int kCacheAttnWarps = kCacheAttnThreads / 32;
 constexpr int kMaxCtas = 8;            // of a cluster
 
-// Rows of a tile: three terms each in NA tiles of 16 stacked rows.
-__host__ __device__ constexpr int cache_attn_rows(int na) { return na * 16 / 3; }
+// Rows of a tile: three terms each in NA tiles of 16 stacked rows, and whole
+// words of four distances.
+__host__ __device__ constexpr int cache_attn_rows(int na) { return na * 4; }
 
 // The tile's split: R rows, `tiles` tiles per (sequence, head), `ctas` per
 // cluster, `cap` keys a CTA holds at once (a multiple of 128).
