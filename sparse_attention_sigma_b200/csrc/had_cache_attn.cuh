@@ -97,7 +97,7 @@ struct WarpStage {
     static constexpr int kStride = D / 2 + 16;
     __align__(16) unsigned char codes[kStages][16 * kStride];
     __align__(8) uint32_t scale[kStages][16];
-    __align__(16) uint32_t terms[2][16 * NA][8];     // bf16 of two neighbouring keys
+    uint4 terms[2][NA][8][4];          // registers of A by lane: [g][t4]
     uint32_t pool_row[kQueue];
     __align__(8) uint32_t dist[(cache_attn_rows(NA) + 3) / 4][kQueue];
 };
@@ -513,7 +513,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 #pragma unroll
     for (int i = 0; i < RWM; ++i) zacc[i] = 0.0f;
     // stacked rows that no term fills stay zero
-    for (int i = lane; i < 2 * 16 * NA * 8; i += 32) (&stage.terms[0][0][0])[i] = 0u;
+    for (int i = lane; i < 2 * NA * 32; i += 32) (&stage.terms[0][0][0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
     // lane r < rows follows row r's level and the ties it may still keep
     const int my_level = lane < rows ? sh.level[lane] : -1;
     int my_quota = lane < rows ? sh.quota[lane] : 0;
@@ -637,11 +637,15 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         // as terms: the upper 8 bits of what is left, twice, and the rest
         auto weigh = [&](int c) {
             const int ring = c % kStages;
-            uint32_t (*const terms)[8] = stage.terms[c & 1];
+            uint32_t *const terms = reinterpret_cast<uint32_t *>(stage.terms[c & 1]);
             const int pair = lane & 7, sub = lane >> 3;
             const uint2 sz = *reinterpret_cast<const uint2 *>(&stage.scale[ring][2 * pair]);
             const float s_a = bf16_lo(sz.x), z_a = fmaf(8.0f, s_a, bf16_hi(sz.x));
             const float s_b = bf16_lo(sz.y), z_b = fmaf(8.0f, s_b, bf16_hi(sz.y));
+            // row x of A and keys 2 pair, 2 pair + 1: a word of lane (x % 8, pair / 2)
+            auto term_word = [&](int x) {
+                return (x >> 4) * 128 + ((x & 7) * 4 + (pair >> 1)) * 4 + (x >> 3 & 1) + 2 * (pair & 1);
+            };
             // a NaN scale must not meet the weight 0 of a row that drops the key
             const bool odd = __any_sync(kFullMask, s_a != s_a || s_b != s_b);
 #pragma unroll
@@ -662,36 +666,41 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                     const float m_b = v_b - __uint_as_float(__float_as_uint(v_b) & 0xffff0000u);
                     const float l_a = m_a - __uint_as_float(__float_as_uint(m_a) & 0xffff0000u);
                     const float l_b = m_b - __uint_as_float(__float_as_uint(m_b) & 0xffff0000u);
-                    terms[r][pair] = __byte_perm(__float_as_uint(v_a), __float_as_uint(v_b), 0x7632);
-                    terms[R + r][pair] = __byte_perm(__float_as_uint(m_a), __float_as_uint(m_b), 0x7632);
-                    terms[2 * R + r][pair] = __byte_perm(__float_as_uint(l_a), __float_as_uint(l_b), 0x7632);
+                    terms[term_word(r)] = __byte_perm(__float_as_uint(v_a), __float_as_uint(v_b), 0x7632);
+                    terms[term_word(R + r)] = __byte_perm(__float_as_uint(m_a), __float_as_uint(m_b), 0x7632);
+                    terms[term_word(2 * R + r)] = __byte_perm(__float_as_uint(l_a), __float_as_uint(l_b), 0x7632);
                 }
             }
         };
-        // Step i issues the copies of chunk i, weighs chunk i - 2 and multiplies
-        // chunk i - 3: the two are independent, and one warp barrier stands
-        // between a step's writes and the next step's reads.
-        for (int step_i = 0;; ++step_i) {
-            while (queued < 16 * (step_i + 1) && k0 < we) look();
-            const int c = step_i - 3;
-            if (c >= 0 && 16 * c >= queued) break;         // (all keys were looked at by then)
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        auto fill = [&](int chunks) {
+            while (queued < 16 * chunks && k0 < we) look();
+        };
+#pragma unroll
+        for (int c = 0; c < kStages - 1; ++c) {
+            fill(c + 1);
             __syncwarp();
-            issue(step_i);
-            if (c < 0) {
-                if (c == -1 && queued > 0) weigh(0);
-                continue;
-            }
+            issue(c);
+        }
+        asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
+        __syncwarp();
+        if (queued > 0) weigh(0);
+        // Step c issues the copies of chunk c + 3, weighs chunk c + 1 and
+        // multiplies chunk c: the last two are independent, and one warp barrier
+        // stands between a step's writes and the next step's reads.
+        for (int c = 0; 16 * c < queued; ++c) {
+            fill(c + kStages);
+            asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 3) : "memory");
+            __syncwarp();
+            issue(c + kStages - 1);
             const int ring = c % kStages;
             // this lane's four keys are 4 t4 .. 4 t4 + 3 and stand for columns
             // 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of A; its codes of a key are
             // elements g D/8 on
             uint32_t af[NA][4], code[4][kCodeWords];
 #pragma unroll
-            for (int i = 0; i < 2 * NA; ++i) {
-                const uint2 u = *reinterpret_cast<const uint2 *>(&stage.terms[c & 1][g + 8 * i][2 * t4]);
-                af[i / 2][i % 2] = u.x;
-                af[i / 2][2 + i % 2] = u.y;
+            for (int m = 0; m < NA; ++m) {
+                const uint4 u = stage.terms[c & 1][m][g][t4];
+                af[m][0] = u.x; af[m][1] = u.y; af[m][2] = u.z; af[m][3] = u.w;
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
