@@ -107,48 +107,59 @@ had_status_t launch_cluster(void (*kernel)(Params...), size_t smem, cudaStream_t
                            args...);
 }
 
-template <typename T, int D, int NA>
-had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, had::CacheAttnPlan plan,
-                                   cudaStream_t st)
+template <int D, int NA, int W>
+had_status_t launch_attention_plan(const had::CacheAttnArgs &a, long long tiles,
+                                   had::CacheAttnPlan plan, long long per, cudaStream_t st)
+{
+    plan.cap = (int)((per + 32 * W - 1) / (32 * W) * (32 * W));
+    if (tiles * plan.ctas > INT_MAX) return HAD_ERR_UNSUPPORTED;
+    plan.by_tiles = had::divisor((unsigned)plan.tiles);
+    plan.by_heads = had::divisor((unsigned)a.c.heads);
+    plan.by_group = had::divisor((unsigned)(a.Hq / a.c.heads));
+    return launch_clusters(had::cache_attn_kernel<D, NA, W>, (unsigned)(tiles * plan.ctas),
+                           (unsigned)plan.ctas, 32 * W,
+                           had::cache_attn_smem_bytes<D, NA, W>(plan), st, a, plan);
+}
+
+template <int D, int NA>
+had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStream_t st)
 {
     const long long rows = (long long)(a.Hq / a.c.heads) * a.T;      // per key-value head
+    had::CacheAttnPlan plan{};
     plan.tiles = (int)((rows + had::cache_attn_rows(NA) - 1) / had::cache_attn_rows(NA));
     plan.R = (int)((rows + plan.tiles - 1) / plan.tiles);
     plan.tiles = (int)((rows + plan.R - 1) / plan.R);
+    plan.ctas = 1;
     // the most keys a tile may see: the device alone knows the lengths
     long long keys = (long long)a.max_pages << a.c.page_log;
     if (a.window > 0) {
         const long long seen = (long long)a.window + a.sinks + plan.R;
         keys = seen < keys ? seen : keys;
     }
+    const long long tiles = (long long)B * a.c.heads * plan.tiles;
+    const int key_bytes = had::cache_attn_key_bytes(plan.R);
+    // Tiles enough for every warp of the card, each short enough for two: CTAs
+    // of two warps, which wait for one another less (CHUNK1).
+    if (tiles >= 14 * 148 && keys * key_bytes <= 12 * 1024)
+        return launch_attention_plan<D, NA, 2>(a, tiles, plan, keys, st);
     // 20 KB of distances at once, so that four CTAs share an SM
-    const long long most = 20 * 1024 / had::cache_attn_key_bytes(plan.R) / 128 * 128;
+    const long long most = 20 * 1024 / key_bytes / 128 * 128;
     // CTAs until four per SM are busy, each with 512 keys or more, and until a
     // CTA holds its slice whole (a longer one is gone through twice)
-    const long long tiles = (long long)B * a.c.heads * plan.tiles;
-    plan.ctas = 1;
     while (plan.ctas < had::kMaxCtas &&
            (keys > most * plan.ctas ||
             (tiles * plan.ctas * 2 <= 4 * 148 && keys > 512LL * plan.ctas)))
         plan.ctas *= 2;
-    const long long per = (keys + 128 * plan.ctas - 1) / (128 * plan.ctas) * 128;
-    plan.cap = (int)(per < most ? per : most);
-    if (tiles * plan.ctas > INT_MAX) return HAD_ERR_UNSUPPORTED;
-    plan.by_tiles = had::divisor((unsigned)plan.tiles);
-    plan.by_heads = had::divisor((unsigned)a.c.heads);
-    plan.by_group = had::divisor((unsigned)(a.Hq / a.c.heads));
-    return launch_clusters(had::cache_attn_kernel<T, D, NA>, (unsigned)(tiles * plan.ctas),
-                           (unsigned)plan.ctas, had::kCacheAttnThreads,
-                           had::cache_attn_smem_bytes<D, NA>(plan), st, a, plan);
+    const long long per = (keys + plan.ctas - 1) / plan.ctas;
+    return launch_attention_plan<D, NA, 4>(a, tiles, plan, per < most ? per : most, st);
 }
 
-template <typename T, int D>
+template <int D>
 had_status_t launch_attention(const had::CacheAttnArgs &a, int B, cudaStream_t st)
 {
-    const had::CacheAttnPlan plan{};
     return (long long)(a.Hq / a.c.heads) * a.T <= had::cache_attn_rows(1)
-               ? launch_attention_tile<T, D, 1>(a, B, plan, st)
-               : launch_attention_tile<T, D, 2>(a, B, plan, st);
+               ? launch_attention_tile<D, 1>(a, B, st)
+               : launch_attention_tile<D, 2>(a, B, st);
 }
 
 unsigned grid_for(long long items, int per_block)
@@ -256,13 +267,9 @@ had_status_t had_cache_attention(const void *Q, had_dtype_t dt, const float *sig
     if (!good(Q, 16) || !good(out, 16) || !good(sigma_q, 4) || !good(lens, 4) ||
         !aligned(counts, 4) || !aligned(dev_status, 4))
         return HAD_ERR_INVALID_ARG;
-    const had::CacheAttnArgs a{Q, sigma_q, c, table, lens, counts, max_pages, Hq, T, N, window,
+    const had::CacheAttnArgs a{Q, dt == HAD_BF16, sigma_q, c, table, lens, counts, max_pages, Hq, T, N, window,
                                sinks, tau, out, dev_status};
-    if (dt == HAD_BF16)
-        return cache->d == 64 ? launch_attention<__nv_bfloat16, 64>(a, B, stream)
-                              : launch_attention<__nv_bfloat16, 128>(a, B, stream);
-    return cache->d == 64 ? launch_attention<float, 64>(a, B, stream)
-                          : launch_attention<float, 128>(a, B, stream);
+    return cache->d == 64 ? launch_attention<64>(a, B, stream) : launch_attention<128>(a, B, stream);
 }
 
 had_status_t had_cache_fork(int32_t *table, int32_t *lens, int32_t *refs, int S, int max_pages,

@@ -26,7 +26,7 @@
 //   4. Per 16 queued keys, behind their copies: the tile's P V on the tensor core.  The codes are
 //      whole numbers below 16, exact in bf16; the weights p s are fp32 and are
 //      cut into three bf16 terms, which hold all 24 bits, and stacked as rows
-//      of A: row x = term R + r.  So the product is as exact as fp32 and any
+//      of A: row x = 4 NA term + r.  So the product is as exact as fp32 and any
 //      scale keeps its exponent.  The product takes c - 8 in place of c; the
 //      rest, p (z + 8 s), is summed beside it.
 //   5. Warps, terms and CTAs are added in a fixed order.
@@ -42,6 +42,7 @@ namespace cg = cooperative_groups;
 
 struct CacheAttnArgs {
     const void *Q;
+    bool q_bf16;                       // else fp32
     const float *sigma;
     CacheView c;
     const int32_t *table, *lens, *counts;
@@ -65,8 +66,6 @@ __device__ __forceinline__ RowRange row_range(const CacheAttnArgs &a, int len, i
     return r;
 }
 
-constexpr int kCacheAttnThreads = 128;
-constexpr int kCacheAttnWarps = kCacheAttnThreads / 32;
 constexpr int kMaxCtas = 8;            // of a cluster
 
 // Rows of a tile: three terms each in NA tiles of 16 stacked rows, and whole
@@ -74,7 +73,7 @@ constexpr int kMaxCtas = 8;            // of a cluster
 __host__ __device__ constexpr int cache_attn_rows(int na) { return na * 4; }
 
 // The tile's split: R rows, `tiles` tiles per (sequence, head), `ctas` per
-// cluster, `cap` keys a CTA holds at once (a multiple of 128).
+// cluster, `cap` keys a CTA of W warps holds at once (a multiple of 32 W).
 struct CacheAttnPlan {
     int R, tiles, ctas, cap;
     Divisor by_tiles, by_heads, by_group;      // of tiles, heads, query heads per head
@@ -119,12 +118,12 @@ __device__ __forceinline__ int sum_swizzle(int n)
     return D == 128 ? n >> 1 : n >> 2;
 }
 
-template <int D, int NA>
+template <int D, int NA, int W>
 size_t cache_attn_smem_bytes(const CacheAttnPlan &p)
 {
-    const size_t keys = sizeof(WarpStage<D, NA>) * kCacheAttnWarps +
+    const size_t keys = sizeof(WarpStage<D, NA>) * W +
                         (size_t)p.cap * cache_attn_key_bytes(p.R) + cache_attn_pages(p.cap) * 4;
-    const size_t red = sizeof(float) * kCacheAttnWarps * 16 * NA * kSumStride<D>;
+    const size_t red = sizeof(float) * W * 16 * NA * kSumStride<D>;
     return keys > red ? keys : red;
 }
 
@@ -164,11 +163,10 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 // codes stay near zero, those of c itself would grow with every key and lose
 // bits on the way (16 k keys, N 2048: relative error 3.3e-6 instead of
 // CENTRED).
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t x)
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t x, uint32_t bias)
 {
-    const uint32_t biased = (x & 0x000f000fu) | 0x43004300u;
     uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(biased), "r"(0x43084308u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"((x & 0x000f000fu) | bias), "r"(0x43084308u));
     return r;
 }
 
@@ -182,7 +180,7 @@ __device__ __forceinline__ uint32_t bytes_below(uint32_t a, uint32_t b)
     return spread;
 }
 
-template <int D, int NA>
+template <int D, int NA, int W>
 struct CacheAttnShared {
     static constexpr int RM = cache_attn_rows(NA);
     __align__(16) uint32_t qbits[RM][D / 32];
@@ -194,21 +192,22 @@ struct CacheAttnShared {
     };
     int level[RM], quota[RM];
     int ranked;                        // some row keeps only part of its ties
-    int ties[kCacheAttnWarps][RM];
-    float zsum[kCacheAttnWarps][RM];
+    int ties[W][RM];
+    float zsum[W][RM];
 };
 
-template <typename T, int D, int NA>
-__global__ void __launch_bounds__(kCacheAttnThreads, NA * D <= 64 ? 5 : NA * D <= 128 ? 4 : 2)
+template <int D, int NA, int W>
+__global__ void __launch_bounds__(32 * W, 4 / W * (NA * D <= 64 ? 5 : NA * D <= 128 ? 4 : 2))
 cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 {
-    constexpr int DW = D / 32;
+    constexpr int kThreads = 32 * W, DW = D / 32;
     constexpr int kTiles = D / 8;             // 8-wide column tiles of the value
     constexpr int kCodeWords = D / 64;        // 32-bit words of codes per lane and key
+    constexpr int RM = cache_attn_rows(NA);
     constexpr int RWM = (cache_attn_rows(NA) + 3) / 4;        // most words of four row bytes
     constexpr uint32_t kNoRow = 0xffffffffu, kUnseen = D + 1, kUnseen4 = kUnseen * 0x01010101u;
     constexpr int KU = 4;                     // keys per lane of one step of the distances
-    using Shared = CacheAttnShared<D, NA>;
+    using Shared = CacheAttnShared<D, NA, W>;
     extern __shared__ __align__(16) unsigned char attn_smem[];
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -216,7 +215,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     using Stage = WarpStage<D, NA>;
     Stage &stage = reinterpret_cast<Stage *>(attn_smem)[warp];
     uint32_t *const distw = reinterpret_cast<uint32_t *>(                    // [RW][cap]
-        attn_smem + sizeof(Stage) * kCacheAttnWarps);
+        attn_smem + sizeof(Stage) * W);
     uint32_t *const page_row = distw + RW * cap;                             // first row of a page
 
     const int C = plan.ctas;
@@ -237,19 +236,21 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     };
     int len = __ldg(a.lens + b), count = a.counts ? __ldg(a.counts + b) : a.T;
     {
-        constexpr int kMine = (cache_attn_rows(NA) + kCacheAttnWarps - 1) / kCacheAttnWarps;
+        constexpr int kMine = (cache_attn_rows(NA) + W - 1) / W;
         float x[kMine][DW], sigma[kMine];
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            const int r = min(warp + i * kCacheAttnWarps, rows - 1);
-            const T *from = static_cast<const T *>(a.Q) + q_row(r) * D + lane;
+            const int r = min(warp + i * W, rows - 1);
+            const long long at = q_row(r) * D + lane;
             sigma[i] = __ldg(a.sigma + h * G + row0 + r - token_of(r) * G);
 #pragma unroll
-            for (int w = 0; w < DW; ++w) x[i][w] = (float)from[32 * w];
+            for (int w = 0; w < DW; ++w)
+                x[i][w] = a.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.Q)[at + 32 * w])
+                                   : static_cast<const float *>(a.Q)[at + 32 * w];
         }
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            const int r = warp + i * kCacheAttnWarps;
+            const int r = warp + i * W;
             if (r >= rows) break;
             const SignRule rule = sign_rule(sigma[i]);
             if (rule.bad && lane == 0) flag(a.status, HAD_ERR_BAD_SIGMA);
@@ -261,7 +262,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         }
         if (tid == 0) sh.ranked = 0;
     }
-    for (int i = tid; i < R * (D + 2); i += kCacheAttnThreads) (&sh.hist[0][0])[i] = 0;
+    for (int i = tid; i < R * (D + 2); i += kThreads) (&sh.hist[0][0])[i] = 0;
     if (len < 0 || len > (long long)a.max_pages << lg || count < 0 || count > a.T) {
         if (tid == 0) flag(a.status, HAD_ERR_INVALID_ARG);
         len = count = 0;
@@ -300,7 +301,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     auto load_pages = [&](int s0, int n) {
         if (n <= 0) return;
         const int first = page_at(s0), last = page_at(s0 + n - 1);
-        for (int i = first + tid; i <= last; i += kCacheAttnThreads) {
+        for (int i = first + tid; i <= last; i += kThreads) {
             const int page = __ldg(table + (i < first_pages ? i : i - to_page));
             const bool there = page >= 0 && page < a.c.pages;
             if (!there) flag(a.status, HAD_ERR_INVALID_ARG);
@@ -395,7 +396,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         }
     };
     // a warp's part of n keys: whole groups of 32, in key order
-    auto warp_begin = [&](int n, int w) { return min(n, w * (((n + kCacheAttnThreads - 1) / kCacheAttnThreads) * 32)); };
+    auto warp_begin = [&](int n, int w) { return min(n, w * (((n + kThreads - 1) / kThreads) * 32)); };
 
     for (int seg = 0; seg < segs; ++seg) {
         const int s0 = u0 + seg * cap, n = min(cap, u1 - s0);
@@ -409,7 +410,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     else __syncthreads();
 
     // level, quota and weights: a warp per row, EL consecutive levels per lane
-    for (int r = warp; r < rows; r += kCacheAttnWarps) {
+    for (int r = warp; r < rows; r += W) {
         constexpr int EL = (D + 2 + 31) / 32;
         int cnt[EL], before[EL], sum = 0;
 #pragma unroll
@@ -503,6 +504,8 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     __syncthreads();
 
     const int g = lane >> 2, t4 = lane & 3;
+    uint32_t bias;                            // one register for all 32 uses of a chunk
+    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(bias));
     float acc[NA][kTiles][4], zacc[RWM];
 #pragma unroll
     for (int m = 0; m < NA; ++m)
@@ -548,7 +551,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         }
         __syncthreads();
         if (lane < rows) {
-            for (int w = 0; w < kCacheAttnWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const int x = sh.ties[w][lane];
                 before += w < warp ? x : 0;
                 all += x;
@@ -637,15 +640,14 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         // as terms: the upper 8 bits of what is left, twice, and the rest
         auto weigh = [&](int c) {
             const int ring = c % kStages;
-            uint32_t *const terms = reinterpret_cast<uint32_t *>(stage.terms[c & 1]);
+            uint32_t *const terms = reinterpret_cast<uint32_t *>(stage.terms[c & 1]) +
+                                    16 * (lane >> 3) + 4 * ((lane & 7) >> 1) + 2 * (lane & 1);
             const int pair = lane & 7, sub = lane >> 3;
             const uint2 sz = *reinterpret_cast<const uint2 *>(&stage.scale[ring][2 * pair]);
             const float s_a = bf16_lo(sz.x), z_a = fmaf(8.0f, s_a, bf16_hi(sz.x));
             const float s_b = bf16_lo(sz.y), z_b = fmaf(8.0f, s_b, bf16_hi(sz.y));
             // row x of A and keys 2 pair, 2 pair + 1: a word of lane (x % 8, pair / 2)
-            auto term_word = [&](int x) {
-                return (x >> 4) * 128 + ((x & 7) * 4 + (pair >> 1)) * 4 + (x >> 3 & 1) + 2 * (pair & 1);
-            };
+            auto term_word = [](int x) { return (x >> 4) * 128 + (x & 7) * 16 + (x >> 3 & 1); };
             // a NaN scale must not meet the weight 0 of a row that drops the key
             const bool odd = __any_sync(kFullMask, s_a != s_a || s_b != s_b);
 #pragma unroll
@@ -666,9 +668,9 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                     const float m_b = v_b - __uint_as_float(__float_as_uint(v_b) & 0xffff0000u);
                     const float l_a = m_a - __uint_as_float(__float_as_uint(m_a) & 0xffff0000u);
                     const float l_b = m_b - __uint_as_float(__float_as_uint(m_b) & 0xffff0000u);
-                    terms[term_word(r)] = __byte_perm(__float_as_uint(v_a), __float_as_uint(v_b), 0x7632);
-                    terms[term_word(R + r)] = __byte_perm(__float_as_uint(m_a), __float_as_uint(m_b), 0x7632);
-                    terms[term_word(2 * R + r)] = __byte_perm(__float_as_uint(l_a), __float_as_uint(l_b), 0x7632);
+                    terms[term_word(4 * i)] = __byte_perm(__float_as_uint(v_a), __float_as_uint(v_b), 0x7632);
+                    terms[term_word(RM + 4 * i)] = __byte_perm(__float_as_uint(m_a), __float_as_uint(m_b), 0x7632);
+                    terms[term_word(2 * RM + 4 * i)] = __byte_perm(__float_as_uint(l_a), __float_as_uint(l_b), 0x7632);
                 }
             }
         };
@@ -722,7 +724,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                     const uint32_t x1 = __byte_perm(code[2][w], code[3][w], sel);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t b0 = codes_bf16(x0 >> (4 * i)), b1 = codes_bf16(x1 >> (4 * i));
+                        const uint32_t b0 = codes_bf16(x0 >> (4 * i), bias), b1 = codes_bf16(x1 >> (4 * i), bias);
 #pragma unroll
                         for (int m = 0; m < NA; ++m) mma_bf16(acc[m][8 * w + 4 * half + i], af[m], b0, b1);
                     }
@@ -744,7 +746,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int x = 16 * m + g + 8 * (e / 2), n = 2 * t4 + e % 2;
-            if (x >= 3 * R) continue;
+            if (x >= 3 * RM) continue;
             float *to = sums + (warp * 16 * NA + x) * kStride + n * kTiles;
 #pragma unroll
             for (int i = 0; i < kTiles; i += 4)
@@ -755,19 +757,19 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     for (int i = 0; i < RWM; ++i)
         if ((lane & 7) == 0 && 4 * i + (lane >> 3) < rows) sh.zsum[warp][4 * i + (lane >> 3)] = zacc[i];
     __syncthreads();
-    for (int e = tid; e < rows * D; e += kCacheAttnThreads) {
+    for (int e = tid; e < rows * D; e += kThreads) {
         const int r = e / D, k = e % D, n = k / kTiles, i = k % kTiles;
         const float *from = sums + r * kStride + n * kTiles + ((i / 4) ^ sum_swizzle<D>(n)) * 4 + i % 4;
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kCacheAttnWarps; ++w, from += 16 * NA * kStride)
-            sum += (from[2 * R * kStride] + from[R * kStride] + sh.zsum[w][r]) + from[0];
+        for (int w = 0; w < W; ++w, from += 16 * NA * kStride)
+            sum += (from[2 * RM * kStride] + from[RM * kStride] + sh.zsum[w][r]) + from[0];
         if (C > 1) sh.part[r][k] = sum;
         else a.out[q_row(r) * D + k] = sum;
     }
     if (C > 1) {
         cluster.sync();
-        for (int e = rank * kCacheAttnThreads + tid; e < rows * D; e += C * kCacheAttnThreads) {
+        for (int e = rank * kThreads + tid; e < rows * D; e += C * kThreads) {
             const int r = e / D, k = e % D;
             float sum = 0.0f;
             for (int o = 0; o < C; ++o) sum += *cluster.map_shared_rank(&sh.part[r][k], o);
