@@ -691,6 +691,15 @@ def test_refusals_of_the_binding(cache):
             (dict(dev_status=torch.zeros(2, dtype=I, device="cuda")), ValueError)):
         with pytest.raises(error):
             cache.had_cache_attention(**dict(ok, **change))
+    for name in ("q", "sigma_q", "table", "lens"):              # a host tensor among the others
+        with pytest.raises(ValueError, match="no CPU path"):
+            cache.had_cache_attention(**dict(ok, **{name: ok[name].cpu()}))
+    for change in (dict(N=2 ** 31), dict(N=-2 ** 31 - 1), dict(window=2 ** 32 + 4), dict(sinks=2 ** 70)):
+        with pytest.raises(ValueError, match="32 bits"):
+            cache.had_cache_attention(**dict(ok, **change))
+    for change in (dict(N=4.5), dict(tau="x"), dict(N=None)):
+        with pytest.raises(TypeError):
+            cache.had_cache_attention(**dict(ok, **change))
     k = torch.zeros(1, 2, 1, 64, device="cuda")
     with pytest.raises(ValueError):
         cache.had_cache_append(k[:, :1].contiguous(), k, s[:2], f.cache, f.table, ints([0]))

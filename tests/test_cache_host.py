@@ -14,13 +14,41 @@ from sparse_attention_sigma_b200 import build as _build
 _build.build()                      # the library loads without a GPU
 from sparse_attention_sigma_b200 import cache  # noqa: E402
 
-lib = cache._lib
 FAKE = 4096                         # never dereferenced: the checks fail first
 OK, INVALID, UNSUPPORTED = 0, 1, 2
 
 
+class PoolStruct(ctypes.Structure):
+    """had_cache_t"""
+    _fields_ = [("kbits", ctypes.c_void_p), ("vcodes", ctypes.c_void_p),
+                ("vscale", ctypes.c_void_p), ("pages", ctypes.c_int), ("heads", ctypes.c_int),
+                ("page", ctypes.c_int), ("d", ctypes.c_int)]
+
+
+def _library():
+    lib = ctypes.CDLL(_build.LIB)
+    vp, i32, f32, pl = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.POINTER(PoolStruct)
+    for name, args in {
+            "had_cache_append": [vp, vp, i32, vp, pl, vp, i32, vp, vp, i32, i32, vp, vp],
+            "had_cache_read": [pl, vp, i32, vp, vp, i32, i32, vp, vp, vp, vp],
+            "had_cache_attention": [vp, i32, vp, pl, vp, i32, vp, vp, i32, i32, i32, i32, f32, i32,
+                                    i32, vp, vp, vp],
+            "had_cache_fork": [vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp, vp],
+            "had_cache_reserve": [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp],
+            "had_cache_free": [vp, vp, vp, i32, i32, i32, vp, i32, vp, vp],
+            "had_cache_evict": [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp],
+            "had_cache_compact": [vp, vp, i32, i32, i32, vp, vp, vp, vp, vp],
+            "had_cache_copy_pages": [pl, vp, vp, i32, vp, vp]}.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
+    return lib
+
+
+lib = _library()
+
+
 def pool(pages=8, heads=2, page=16, d=64, kbits=FAKE, vcodes=FAKE, vscale=FAKE):
-    return ctypes.byref(cache._Pool(kbits, vcodes, vscale, pages, heads, page, d))
+    return ctypes.byref(PoolStruct(kbits, vcodes, vscale, pages, heads, page, d))
 
 
 def call(name, ok, **changes):
@@ -115,28 +143,13 @@ K = torch.zeros(1, 2, 3, 64)
 TABLE, VEC, REFS = torch.zeros(1, 4, dtype=I), torch.zeros(1, dtype=I), torch.zeros(8, dtype=I)
 
 
-class HostCache(cache.Cache):
-    """A Cache over host tensors, to reach the checks of the other arguments."""
-
-    def __init__(self):
-        self.pages, self.heads, self.page, self.d = 8, 2, 16, 64
-        self.device = torch.device("cpu")
-        self._pool = cache._Pool(FAKE, FAKE, FAKE, 8, 2, 16, 64)
-
-
-HOST = HostCache()
 CALLS = {
     "Cache": lambda: cache.Cache(*[torch.zeros(1, 1, 16, 2, dtype=I)] * 3),
-    "had_cache_append": lambda: cache.had_cache_append(K, K, torch.ones(2), HOST, TABLE, VEC),
-    "had_cache_read": lambda: cache.had_cache_read(HOST, TABLE, VEC, 3),
-    "had_cache_attention": lambda: cache.had_cache_attention(K, torch.ones(2), HOST, TABLE, VEC, 2,
-                                                             0.1),
     "had_cache_fork": lambda: cache.had_cache_fork(TABLE, VEC, REFS, 16, VEC, VEC),
     "had_cache_reserve": lambda: cache.had_cache_reserve(TABLE, VEC, REFS, 16, VEC),
     "had_cache_free": lambda: cache.had_cache_free(TABLE, VEC, REFS, VEC),
     "had_cache_evict": lambda: cache.had_cache_evict(TABLE, VEC, REFS, 16, 8),
     "had_cache_compact": lambda: cache.had_cache_compact(TABLE, REFS),
-    "had_cache_copy_pages": lambda: cache.had_cache_copy_pages(HOST, VEC, VEC),
 }
 
 
@@ -146,16 +159,36 @@ def test_host_tensors_are_refused(name):
         CALLS[name]()
 
 
+# a Cache holds device tensors, so these can only be reached with one: on a host
+# they refuse whatever else they are given
+NEED_A_CACHE = {
+    "had_cache_append": lambda c: cache.had_cache_append(K, K, torch.ones(2), c, TABLE, VEC),
+    "had_cache_read": lambda c: cache.had_cache_read(c, TABLE, VEC, 3),
+    "had_cache_attention": lambda c: cache.had_cache_attention(K, torch.ones(2), c, TABLE, VEC, 2,
+                                                               0.1),
+    "had_cache_copy_pages": lambda c: cache.had_cache_copy_pages(c, VEC, VEC),
+}
+
+
+@pytest.mark.parametrize("name", sorted(NEED_A_CACHE))
+def test_what_is_no_cache_is_refused(name):
+    for c in (None, K, object()):
+        with pytest.raises(TypeError, match="Cache"):
+            NEED_A_CACHE[name](c)
+
+
 def test_every_wrapper_is_covered():
     public = {n for n in dir(cache) if n.startswith("had_") and callable(getattr(cache, n))}
-    assert public <= set(CALLS), public - set(CALLS)
+    assert public <= set(CALLS) | set(NEED_A_CACHE), public
 
 
-def test_numbers_beyond_32_bits_are_refused():
-    for x in (2 ** 31, -2 ** 31 - 1, 2 ** 32 + 4):
-        with pytest.raises(ValueError, match="32 bits"):
-            cache._int(x, "N")
-    assert cache._int(2 ** 31 - 1, "N") == 2 ** 31 - 1
+def test_wrong_objects_are_refused():
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        cache.had_cache_compact([[0]], REFS)
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        cache.Cache(None, None, None)
+    with pytest.raises(TypeError, match="stream"):
+        cache.had_cache_compact(TABLE, REFS, stream=3)
 
 
 def test_cache_empty_refuses_sizes_the_library_lacks():
@@ -163,8 +196,6 @@ def test_cache_empty_refuses_sizes_the_library_lacks():
         cache.Cache.empty(4, 1, 16, 96)
     with pytest.raises(ValueError, match="page must be"):
         cache.Cache.empty(4, 1, 24, 64)
-    with pytest.raises(TypeError, match="Cache"):
-        cache.had_cache_copy_pages(None, VEC, VEC)
 
 
 # ---------------------------------------------------------- pins of the oracle
