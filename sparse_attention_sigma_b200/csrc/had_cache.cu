@@ -186,12 +186,12 @@ had_status_t check_rows(int B, int heads, int T)
     return bh > INT_MAX || bh * T > INT_MAX ? HAD_ERR_UNSUPPORTED : HAD_OK;
 }
 
-// Rows (b, head, token) of an append or a read, and the grid that has 16
-// lanes for kCacheRows of them.
+// Rows (b, head, token) of an append or a read, and the grid that has `lanes`
+// threads for kCacheRows of them.
 CacheTokens tokens_of(const int32_t *table, int max_pages, const int32_t *start,
-                      const int32_t *counts, int B, int heads, int T, unsigned *grid)
+                      const int32_t *counts, int B, int heads, int T, int lanes, unsigned *grid)
 {
-    const unsigned rows = (unsigned)B * heads * T, per = 256 / had::kCacheLanes * had::kCacheRows;
+    const unsigned rows = (unsigned)B * heads * T, per = 256 / lanes * had::kCacheRows;
     *grid = (rows + per - 1) / per;
     return CacheTokens{table, start, counts, max_pages, T, rows, had::divisor(T),
                        had::divisor(heads)};
@@ -218,7 +218,8 @@ had_status_t had_cache_append(const void *K, const void *V, had_dtype_t dt, cons
         !aligned(counts, 4) || !aligned(dev_status, 4))
         return HAD_ERR_INVALID_ARG;
     unsigned grid;
-    const CacheTokens k = tokens_of(table, max_pages, start, counts, B, c.heads, T, &grid);
+    const CacheTokens k = tokens_of(table, max_pages, start, counts, B, c.heads, T,
+                                    had::kCacheLanes, &grid);
     if (dt == HAD_BF16)
         launch_append<__nv_bfloat16>(K, V, sigma_k, c, cache->d, k, grid, dev_status, stream);
     else
@@ -241,7 +242,8 @@ had_status_t had_cache_read(const had_cache_t *cache, const int32_t *table, int 
         return HAD_ERR_INVALID_ARG;
     if (!bits && !values) return HAD_ERR_INVALID_ARG;
     unsigned grid;
-    const CacheTokens k = tokens_of(table, max_pages, start, counts, B, c.heads, T, &grid);
+    const CacheTokens k = tokens_of(table, max_pages, start, counts, B, c.heads, T,
+                                    had::kReadLanes, &grid);
     if (cache->d == 64)
         had::cache_read_kernel<64><<<grid, 256, 0, stream>>>(c, k, bits, values, dev_status);
     else
@@ -359,8 +361,9 @@ had_status_t had_cache_copy_pages(const had_cache_t *cache, const int32_t *src,
     if (n == 0) return HAD_OK;
     if (!good(src, 4) || !good(dst, 4) || !aligned(dev_status, 4)) return HAD_ERR_INVALID_ARG;
     const long long rows = (long long)c.heads * cache->page, d = cache->d;
-    had::cache_copy_kernel<<<dim3(4, n < 65535 ? n : 65535), 256, 0, stream>>>(
-        c, rows * d / 128, rows * d / 32, rows / 4, src, dst, n, dev_status);
+    const had::CopyWords words{rows * d / 32, rows * d / 128, rows / 4};
+    had::cache_copy_kernel<<<dim3(had::kCopyParts, n < 512 ? n : 512), 256, 0, stream>>>(
+        c, words, src, dst, n, dev_status);
     return launched();
 }
 

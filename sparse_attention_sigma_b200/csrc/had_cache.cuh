@@ -25,11 +25,12 @@ struct CacheView {
     int page_log;          // log2 of the tokens of a page
 };
 
-// Row of (page, head, slot) in the three arrays; 64 bits, a pool may hold
-// more than 2^31 rows.
-__device__ __forceinline__ long long cache_row(const CacheView &c, int page, int head, int slot)
+// Row of (page, head, slot) in the three arrays: below 2^32 - 1 in every pool.
+constexpr uint32_t kNoRow = 0xffffffffu;
+
+__device__ __forceinline__ uint32_t cache_row(const CacheView &c, int page, int head, int slot)
 {
-    return (((long long)page * c.heads + head) << c.page_log) + slot;
+    return (((unsigned)page * (unsigned)c.heads + (unsigned)head) << c.page_log) + (unsigned)slot;
 }
 
 // The largest bf16 not above the finite x, as fp32: cut towards zero, and one
@@ -42,19 +43,54 @@ __device__ __forceinline__ float bf16_down(float x)
     return __uint_as_float(cut);
 }
 
-// min and max that give NaN when an operand is NaN
-__device__ __forceinline__ float min_nan(float a, float b)
+// min and max of three that give NaN when an operand is NaN
+__device__ __forceinline__ float min_nan(float a, float b, float c)
 {
     float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
-__device__ __forceinline__ float max_nan(float a, float b)
+__device__ __forceinline__ float max_nan(float a, float b, float c)
 {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// Two fp32 values that take one instruction together, each rounded as alone.
+struct Two {
+    unsigned long long raw;
+    __device__ __forceinline__ Two(float a, float b)
+    {
+        asm("mov.b64 %0, {%1, %2};" : "=l"(raw) : "f"(a), "f"(b));
+    }
+    __device__ __forceinline__ explicit Two(unsigned long long r) : raw(r) {}
+    __device__ __forceinline__ void get(float &a, float &b) const
+    {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(raw));
+    }
+};
+
+__device__ __forceinline__ Two operator+(Two a, Two b)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.raw), "l"(b.raw));
+    return Two(r);
+}
+
+__device__ __forceinline__ Two operator*(Two a, Two b)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a.raw), "l"(b.raw));
+    return Two(r);
+}
+
+__device__ __forceinline__ Two fma(Two a, Two b, Two c)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a.raw), "l"(b.raw), "l"(c.raw));
+    return Two(r);
 }
 
 // Division of n < 2^31 by a divisor known on the host, with the multiplier
@@ -77,7 +113,7 @@ __device__ __forceinline__ unsigned divide(unsigned n, const Divisor &d)
     return (__umulhi(n, d.mul) + n) >> d.shift;
 }
 
-constexpr int kCacheLanes = 16;        // threads of one (token, head) row
+constexpr int kCacheLanes = 8;         // threads of one (token, head) row
 constexpr int kCacheRows = 2;          // rows of a thread whose loads are in flight together
 
 // Where the tokens of an append or a read lie: row i of rows = (b, head, t).
@@ -108,23 +144,23 @@ __device__ __forceinline__ CacheToken cache_token(const CacheTokens &k, unsigned
     return x;
 }
 
-// Row of the pool that holds a real token, -1 where the table has no place for it.
-__device__ __forceinline__ long long cache_place(const CacheView &c, const CacheTokens &k,
+// Row of the pool that holds a real token, none where the table has no place for it.
+__device__ __forceinline__ uint32_t cache_place(const CacheView &c, const CacheTokens &k,
                                                  const CacheToken &x, int32_t *status)
 {
-    if (!x.real) return -1;
+    if (!x.real) return kNoRow;
     const long long pos = (long long)__ldg(k.start + x.b) + x.t;
     int page = -1;
     if (pos >= 0 && pos < (long long)k.max_pages << c.page_log)
         page = __ldg(k.table + (long long)x.b * k.max_pages + (pos >> c.page_log));
     if (page < 0 || page >= c.pages) {
         flag(status, HAD_ERR_INVALID_ARG);
-        return -1;
+        return kNoRow;
     }
     return cache_row(c, page, x.head, (int)(pos & ((1 << c.page_log) - 1)));
 }
 
-// E = 4 or 8 consecutive elements of a row as one or two 16-byte loads.
+// E = 8 or 16 consecutive elements of a row, by 16-byte loads.
 template <typename T, int E>
 struct CacheSlice {
     static constexpr int kWords = sizeof(T) * E / 4;
@@ -132,15 +168,10 @@ struct CacheSlice {
 
     __device__ __forceinline__ void load(const T *p)
     {
-        if constexpr (kWords == 2) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-            raw[0] = u.x; raw[1] = u.y;
-        } else {
 #pragma unroll
-            for (int i = 0; i < kWords; i += 4) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4);
-                raw[i] = u.x; raw[i + 1] = u.y; raw[i + 2] = u.z; raw[i + 3] = u.w;
-            }
+        for (int i = 0; i < kWords; i += 4) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4);
+            raw[i] = u.x; raw[i + 1] = u.y; raw[i + 2] = u.z; raw[i + 3] = u.w;
         }
     }
 
@@ -189,15 +220,18 @@ struct CacheSlice {
 // it sees NaN.
 //
 // HBM-bound once the arithmetic is lean: 2 d elements read, d/8 + d/2 + 4
-// bytes written per row.  16 lanes take a row, so that a bf16 row of d = 128
-// is one 16-byte load per lane, and two rows are in flight; the extremes are
-// joined by four shuffles and a word of signs by the 32 / E lanes that hold its
-// elements (E = d / 16).  The quotients are products with 1 / s (off by less
-// than 2^-18 in all: three roundings of at most 16) and only a slice with one
-// that close to a half divides.  No lane leaves early: the shuffles then name
-// the whole warp, and half-warp masks cost more than all of the arithmetic
-// (measured on 197 k rows of d 128, bf16, with the exact divisions: 80 us
-// against APPEND_US now, 22 us of HBM time).
+// bytes written per row.  8 lanes take a row, two rows are in flight: what a row
+// costs once (place, scale, quotients: about 130 instructions) is shared by
+// E = d / 8 elements a lane.  The extremes are joined by three shuffles and a
+// word of signs by the 32 / E lanes that hold its elements.  Element-wise
+// arithmetic takes two values an instruction.  A quotient is x y with y = 1 / s
+// rounded, corrected once by its exact remainder, which makes it the rounded
+// quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990, theorem 7).  No lane leaves early: the shuffles
+// then name the whole warp, and half-warp masks cost more than all of the
+// arithmetic (197 k rows of d 128, bf16: 80 us so, 57 us with whole warps and 16
+// lanes a row, 46 us with 8 and divisions beside a half, APPEND_US now; 20 us of
+// HBM time).
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
 cache_append_kernel(const T *__restrict__ K, const T *__restrict__ V,
@@ -209,7 +243,7 @@ cache_append_kernel(const T *__restrict__ K, const T *__restrict__ V,
     const unsigned row0 = (blockIdx.x * 256u + threadIdx.x) / kCacheLanes;
     CacheSlice<T, E> key[kCacheRows], value[kCacheRows];
     CacheToken token[kCacheRows];
-    long long at[kCacheRows];
+    uint32_t at[kCacheRows];
     float sg[kCacheRows];
 #pragma unroll
     for (int i = 0; i < kCacheRows; ++i) token[i] = cache_token(k, row0 + i * step, status);
@@ -225,27 +259,28 @@ cache_append_kernel(const T *__restrict__ K, const T *__restrict__ V,
     for (int i = 0; i < kCacheRows; ++i) at[i] = cache_place(c, k, token[i], status);
 #pragma unroll
     for (int i = 0; i < kCacheRows; ++i) {
-        const bool here = at[i] >= 0;
+        const bool here = at[i] != kNoRow;
         const SignRule rule = sign_rule(sg[i]);
         if (rule.bad && l == 0 && here) flag(status, HAD_ERR_BAD_SIGMA);
         uint32_t word = key[i].signs(rule, bf16_kge(rule)) << (E * (l & (kPerWord - 1)));
 #pragma unroll
         for (int o = 1; o < kPerWord; o <<= 1) word |= __shfl_xor_sync(kFullMask, word, o);
-        if (here && (l & (kPerWord - 1)) == 0) c.kbits[at[i] * (D / 32) + l / kPerWord] = word;
+        if (here && (l & (kPerWord - 1)) == 0) c.kbits[(size_t)at[i] * (D / 32) + l / kPerWord] = word;
 
         float v[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = value[i].at(e);
         float lo = v[0], hi = v[0];
 #pragma unroll
-        for (int e = 1; e < E; ++e) {
-            lo = min_nan(lo, v[e]);
-            hi = max_nan(hi, v[e]);
+        for (int e = 1; e < E; e += 2) {
+            lo = min_nan(lo, v[e], v[e + 1 < E ? e + 1 : e]);
+            hi = max_nan(hi, v[e], v[e + 1 < E ? e + 1 : e]);
         }
 #pragma unroll
         for (int o = 1; o < kCacheLanes; o <<= 1) {
-            lo = min_nan(lo, __shfl_xor_sync(kFullMask, lo, o));
-            hi = max_nan(hi, __shfl_xor_sync(kFullMask, hi, o));
+            const float l2 = __shfl_xor_sync(kFullMask, lo, o), h2 = __shfl_xor_sync(kFullMask, hi, o);
+            lo = min_nan(lo, l2, l2);
+            hi = max_nan(hi, h2, h2);
         }
         const float z = bf16_down(lo + 0.0f);         // -0 becomes +0
         const float s = -bf16_down(-__fdiv_rn(hi - z, 15.0f)) + 0.0f;
@@ -256,31 +291,33 @@ cache_append_kernel(const T *__restrict__ K, const T *__restrict__ V,
         // four codes c0 + 16 c1 + 256 c2 + 4096 c3 are a whole number below
         // 2^16, exact in fp32, and the last bits of its sum with 2^23
         constexpr float kWhole = 12582912.0f;         // 1.5 2^23: the sum's last bit is 1
-        float far = 0.0f;
-        uint32_t codes = 0;
+        const Two minus_z(-z, -z), by(inv, inv), up(kWhole, kWhole), down(-kWhole, -kWhole);
+        const Two minus_s(-s, -s);
+        uint32_t codes[E / 8];
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
-            float four = 0.0f;
+            float r[4];
 #pragma unroll
-            for (int f = 3; f >= 0; --f) {
-                const float q = (v[e + f] - z) * inv, r = (q + kWhole) - kWhole;
-                far = fmaxf(far, fabsf(q - r));
-                four = fmaf(four, 16.0f, r);
+            for (int f = 0; f < 4; f += 2) {
+                const Two x = Two(v[e + f], v[e + f + 1]) + minus_z, q = x * by;
+                (fma(fma(q, minus_s, x), by, q) + up + down).get(r[f], r[f + 1]);
             }
-            codes |= (__float_as_uint(four + 8388608.0f) & 0xffffu) << (4 * e);
+            const float four = fmaf(fmaf(r[3], 16.0f, r[2]), 256.0f, fmaf(r[1], 16.0f, r[0]));
+            const uint32_t low = __float_as_uint(four + 8388608.0f);
+            codes[e / 8] = e % 8 ? __byte_perm(codes[e / 8], low, 0x5410) : low;
         }
-        // 1 / s overflows below 2^-128: such rows divide, too
-        if (coded && (!(far < 0.5f - 7.6293945e-6f) || !(inv <= FLT_MAX))) {
-            codes = 0;
+        if (coded && s < 8.077936e-28f) {             // 2^-90: a remainder may be subnormal
 #pragma unroll
-            for (int e = 0; e < E; ++e) codes |= (uint32_t)rintf(__fdiv_rn(v[e] - z, s)) << (4 * e);
+            for (int e = 0; e < E; ++e)
+                codes[e / 8] = (e % 8 ? codes[e / 8] : 0u) |
+                               (uint32_t)rintf(__fdiv_rn(v[e] - z, s)) << (4 * (e % 8));
         }
-        if (!coded) codes = 0;
         if (here) {
-            if constexpr (E == 8)
-                reinterpret_cast<uint32_t *>(c.vcodes)[at[i] * kCacheLanes + l] = codes;
+            uint32_t *const to = reinterpret_cast<uint32_t *>(c.vcodes) + (size_t)at[i] * (D / 8) + l * (E / 8);
+            if constexpr (E == 16)
+                *reinterpret_cast<uint2 *>(to) = coded ? make_uint2(codes[0], codes[1]) : make_uint2(0u, 0u);
             else
-                reinterpret_cast<uint16_t *>(c.vcodes)[at[i] * kCacheLanes + l] = (uint16_t)codes;
+                *to = coded ? codes[0] : 0u;
             if (l == 0)
                 c.vscale[at[i]] = fine ? (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xffff0000u)
                                        : 0x7fc07fc0u;
@@ -290,34 +327,34 @@ cache_append_kernel(const T *__restrict__ K, const T *__restrict__ V,
 
 // Tokens of the cache as packed signs and fp32 values c s + z (one FMA:
 // rounded once); zeros for tokens beyond a sequence's count.  HBM-bound by
-// the 4 d bytes written per row; 16 lanes a row, each E / 4 times 16 bytes of
+// the 4 d bytes written per row; 16 lanes a row, each D / 64 times 16 bytes of
 // consecutive lanes, two rows in flight (READ_US for 262 k rows of d 128, of
-// which 197 k are there; 23 us of HBM time).
+// which 197 k are there; 24 us of HBM time).
+constexpr int kReadLanes = 16;
+
 template <int D>
 __global__ void __launch_bounds__(256)
 cache_read_kernel(CacheView c, CacheTokens k, uint32_t *__restrict__ bits,
                   float *__restrict__ values, int32_t *status)
 {
-    constexpr int E = D / kCacheLanes;
-    const int l = threadIdx.x & (kCacheLanes - 1);
-    const unsigned step = gridDim.x * (256u / kCacheLanes);
-    const unsigned row0 = (blockIdx.x * 256u + threadIdx.x) / kCacheLanes;
-    long long at[kCacheRows];
+    constexpr int E = D / kReadLanes;
+    const int l = threadIdx.x & (kReadLanes - 1);
+    const unsigned step = gridDim.x * (256u / kReadLanes);
+    const unsigned row0 = (blockIdx.x * 256u + threadIdx.x) / kReadLanes;
+    uint32_t at[kCacheRows];
     uint32_t codes[kCacheRows][E / 4], sz[kCacheRows], word[kCacheRows];
 #pragma unroll
-    for (int i = 0; i < kCacheRows; ++i) {
-        const unsigned row = row0 + i * step;
-        at[i] = cache_place(c, k, cache_token(k, row, status), status);
-    }
+    for (int i = 0; i < kCacheRows; ++i)
+        at[i] = cache_place(c, k, cache_token(k, row0 + i * step, status), status);
 #pragma unroll
     for (int i = 0; i < kCacheRows; ++i) {
-        const bool here = at[i] >= 0;
-        word[i] = here && bits && l < D / 32 ? __ldg(c.kbits + at[i] * (D / 32) + l) : 0u;
+        const bool here = at[i] != kNoRow;
+        word[i] = here && bits && l < D / 32 ? __ldg(c.kbits + (size_t)at[i] * (D / 32) + l) : 0u;
         sz[i] = here && values ? __ldg(c.vscale + at[i]) : 0u;
 #pragma unroll
         for (int e = 0; e < E / 4; ++e)
             codes[i][e] = here && values ? __ldg(reinterpret_cast<const uint16_t *>(c.vcodes) +
-                                                 at[i] * (D / 4) + e * kCacheLanes + l) : 0u;
+                                                 (size_t)at[i] * (D / 4) + e * kReadLanes + l) : 0u;
     }
 #pragma unroll
     for (int i = 0; i < kCacheRows; ++i) {
@@ -325,16 +362,17 @@ cache_read_kernel(CacheView c, CacheTokens k, uint32_t *__restrict__ bits,
         if (row >= k.rows) break;
         if (bits && l < D / 32) bits[(long long)row * (D / 32) + l] = word[i];
         if (!values) continue;
-        const float s = bf16_lo(sz[i]), z = bf16_hi(sz[i]);
+        const Two s(bf16_lo(sz[i]), bf16_lo(sz[i])), z(bf16_hi(sz[i]), bf16_hi(sz[i]));
         // 2^23 + c has c in its last bits
-        auto value = [&](uint32_t code) {
-            return fmaf(__uint_as_float((code & 15u) | 0x4b000000u) - 8388608.0f, s, z);
-        };
+        const Two down(-8388608.0f, -8388608.0f);
+        auto raised = [](uint32_t code) { return __uint_as_float((code & 15u) | 0x4b000000u); };
 #pragma unroll
         for (int e = 0; e < E / 4; ++e) {
             const uint32_t x = codes[i][e];
-            float4 f = make_float4(value(x), value(x >> 4), value(x >> 8), value(x >> 12));
-            reinterpret_cast<float4 *>(values + (long long)row * D)[e * kCacheLanes + l] = f;
+            float4 f;
+            fma(Two(raised(x), raised(x >> 4)) + down, s, z).get(f.x, f.y);
+            fma(Two(raised(x >> 8), raised(x >> 12)) + down, s, z).get(f.z, f.w);
+            reinterpret_cast<float4 *>(values + (long long)row * D)[e * kReadLanes + l] = f;
         }
     }
 }

@@ -205,7 +205,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     constexpr int kCodeWords = D / 64;        // 32-bit words of codes per lane and key
     constexpr int RM = cache_attn_rows(NA);
     constexpr int RWM = (cache_attn_rows(NA) + 3) / 4;        // most words of four row bytes
-    constexpr uint32_t kNoRow = 0xffffffffu, kUnseen = D + 1, kUnseen4 = kUnseen * 0x01010101u;
+    constexpr uint32_t kUnseen = D + 1, kUnseen4 = kUnseen * 0x01010101u;
     constexpr int KU = 4;                     // keys per lane of one step of the distances
     using Shared = CacheAttnShared<D, NA, W>;
     extern __shared__ __align__(16) unsigned char attn_smem[];
