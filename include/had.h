@@ -398,7 +398,7 @@ HAD_API size_t had_noalloc_scratch_bytes(void);
  *     page    16, 32, 64, 128 or 256;  d 64 or 128
  *     pages * heads * page < 2^32
  *   table   [S, max_pages] int32 (device): pages of sequence s in order, -1
- *           for none.  max_pages * page < 2^31.
+ *           for none.  max_pages * page < 2^31 - 2^16.
  *   lens    [S] int32: tokens of a sequence;  refs [pages] int32: how many
  *           table entries name a page, 0 = free.  The caller starts them with
  *           -1, 0 and 0.

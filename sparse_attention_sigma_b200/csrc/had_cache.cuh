@@ -230,7 +230,7 @@ struct CacheSlice {
 // System/6000 processor", 1990, theorem 7).  No lane leaves early: the shuffles
 // then name the whole warp, and half-warp masks cost more than all of the
 // arithmetic (197 k rows of d 128, bf16: 80 us so, 57 us with whole warps and 16
-// lanes a row, 46 us with 8 and divisions beside a half, APPEND_US now; 20 us of
+// lanes a row, 46 us with 8 and divisions beside a half, 36 us now; 20 us of
 // HBM time).
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
@@ -328,7 +328,7 @@ cache_append_kernel(const T *__restrict__ K, const T *__restrict__ V,
 // Tokens of the cache as packed signs and fp32 values c s + z (one FMA:
 // rounded once); zeros for tokens beyond a sequence's count.  HBM-bound by
 // the 4 d bytes written per row; 16 lanes a row, each D / 64 times 16 bytes of
-// consecutive lanes, two rows in flight (READ_US for 262 k rows of d 128, of
+// consecutive lanes, two rows in flight (30 us for 262 k rows of d 128, of
 // which 197 k are there; 24 us of HBM time).
 constexpr int kReadLanes = 16;
 

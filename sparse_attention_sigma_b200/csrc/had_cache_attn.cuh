@@ -13,7 +13,7 @@
 //
 // One cluster of CTAs takes a tile of R rows that share a key-value head (its
 // query heads, and neighbouring tokens of a draft or chunk) and splits the keys
-// that any of them sees; a CTA's four warps split its slice, in key order.
+// that any of them sees; a CTA's warps split its slice, in key order.
 //   1. Distances: a lane per key, the key's bits in registers, XOR + popc with
 //      every row's bits from shared memory; 8-bit distances stay in shared
 //      memory (d + 1: not visible), counts go to the CTA's histograms.
@@ -23,14 +23,24 @@
 //   3. Each warp goes through its part again, drops what a row does not keep
 //      (ties by rank in key order) and queues the keys that at least one row
 //      keeps; their codes and scales are copied to shared memory from there.
-//   4. Per 16 queued keys, behind their copies: the tile's P V on the tensor core.  The codes are
-//      whole numbers below 16, exact in bf16; the weights p s are fp32 and are
-//      cut into three bf16 terms, which hold all 24 bits, and stacked as rows
-//      of A: row x = 4 NA term + r.  So the product is as exact as fp32 and any
-//      scale keeps its exponent.  The product takes c - 8 in place of c; the
-//      rest, p (z + 8 s), is summed beside it.
+//   4. Per 16 queued keys, behind their copies: the tile's P V on the tensor
+//      core.  The codes are whole numbers below 16, exact in bf16; the weights
+//      p s are fp32 and are cut into three bf16 terms, which hold all 24 bits,
+//      and stacked as rows of A: row x = 4 NA term + r.  So the product is as
+//      exact as fp32 and any scale keeps its exponent.  The product takes c - 8
+//      in place of c; the rest, p (z + 8 s), is summed beside it.
 //   5. Warps, terms and CTAs are added in a fixed order.
 // The union of the rows' kept keys is read once, each key's bits once.
+//
+// mma.sync and not tcgen05: a tile has 4 or 8 rows of 64 or 128, B is made in
+// registers from gathered codes, and the tensor pipe is 8 % busy.  What bounds
+// it is the issue of the instructions around the product (16 sequences of 16 k
+// tokens, 32 query and 8 key heads, d 128, N 2048: 72 us, 34 M warp
+// instructions, half of all issue slots; 127 MB from memory would take 19 us):
+// about 20 a (row, 32 keys) for distances and selection, 350 per 16 kept keys
+// of d 128, of which 128 unpack and multiply codes, 80 make the weights and 45
+// copy.  16 warps an SM is what the accumulators' registers allow; 20 and 24
+// warps spill (95 and 115 us), 12 hide less (92 us).
 #pragma once
 #include <cooperative_groups.h>
 
@@ -69,7 +79,8 @@ __device__ __forceinline__ RowRange row_range(const CacheAttnArgs &a, int len, i
 constexpr int kMaxCtas = 8;            // of a cluster
 
 // Rows of a tile: three terms each in NA tiles of 16 stacked rows, and whole
-// words of four distances.
+// words of four distances (5 and 10 rows fill the stacked rows better, but the
+// distances worse, and took 2 to 33 % longer).
 __host__ __device__ constexpr int cache_attn_rows(int na) { return na * 4; }
 
 // The tile's split: R rows, `tiles` tiles per (sequence, head), `ctas` per
@@ -162,7 +173,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 // core cuts its running sums, it does not round them; sums of the centred
 // codes stay near zero, those of c itself would grow with every key and lose
 // bits on the way (16 k keys, N 2048: relative error 3.3e-6 instead of
-// CENTRED).
+// 2.2e-7).
 __device__ __forceinline__ uint32_t codes_bf16(uint32_t x, uint32_t bias)
 {
     uint32_t r;
@@ -533,31 +544,31 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         // ties of each row in this warp's part, where a row keeps only some
         int before = 0, all = 0, here = 0;
         if (sh.ranked) {
-        for (int q = 0; q < RW; ++q) {
-            uint32_t same = 0;
+            for (int q = 0; q < RW; ++q) {
+                uint32_t same = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int l = __shfl_sync(kFullMask, my_level, 4 * q + i);
-                same |= (l < 0 ? 0xffu : (uint32_t)l) << (8 * i);
-            }
-            uint32_t mine = 0;                // a byte per row: at most cap / 128 keys a lane
-            for (int k = wb + lane; k < we; k += 32)
-                mine += __vcmpeq4(distw[q * cap + k], same) & 0x01010101u;
+                for (int i = 0; i < 4; ++i) {
+                    const int l = __shfl_sync(kFullMask, my_level, 4 * q + i);
+                    same |= (l < 0 ? 0xffu : (uint32_t)l) << (8 * i);
+                }
+                uint32_t mine = 0;                // a byte per row: at most cap / 128 keys a lane
+                for (int k = wb + lane; k < we; k += 32)
+                    mine += __vcmpeq4(distw[q * cap + k], same) & 0x01010101u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int s = __reduce_add_sync(kFullMask, mine >> (8 * i) & 255u);
-                if (lane == 0 && 4 * q + i < rows) sh.ties[warp][4 * q + i] = s;
+                for (int i = 0; i < 4; ++i) {
+                    const int s = __reduce_add_sync(kFullMask, mine >> (8 * i) & 255u);
+                    if (lane == 0 && 4 * q + i < rows) sh.ties[warp][4 * q + i] = s;
+                }
             }
-        }
-        __syncthreads();
-        if (lane < rows) {
-            for (int w = 0; w < W; ++w) {
-                const int x = sh.ties[w][lane];
-                before += w < warp ? x : 0;
-                all += x;
-                here = w == warp ? x : here;
+            __syncthreads();
+            if (lane < rows) {
+                for (int w = 0; w < W; ++w) {
+                    const int x = sh.ties[w][lane];
+                    before += w < warp ? x : 0;
+                    all += x;
+                    here = w == warp ? x : here;
+                }
             }
-        }
         }
         // keep bytes below `limit`; a row whose quota ends inside this part
         // keeps its first `left` ties

@@ -186,6 +186,33 @@ def test_append_of_special_rows(cache):
     assert flags(st) == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_codes_of_many_rows_are_those_of_the_ieee_quotient(cache, dtype, d):
+    """Quotients beside and on a half: rows of few bits, of whole multiples of half a step, of any
+    magnitude down to subnormal scales."""
+    g = torch.Generator().manual_seed(d)
+    T = 16384
+    v = torch.randn(1, 1, T, d, generator=g)
+    kind = torch.arange(T)[:, None] % 4
+    v = torch.where(kind == 1, (v * 8).round() / 8, v)
+    half = torch.randint(0, 31, (T, d), generator=g) * 0.5
+    half[:, 0], half[:, 1] = 0, 15
+    v = torch.where(kind == 2, half * (1 + torch.randint(0, 128, (T, 1), generator=g) / 128), v)
+    v = torch.where(kind == 3, v * 2.0 ** torch.randint(-148, 120, (T, 1), generator=g), v).to(dtype)
+    c = cache.Cache.empty(T // 256, 1, 256, d)
+    st = status()
+    cache.had_cache_append(v.cuda(), v.cuda(), torch.ones(1, device="cuda"), c,
+                           torch.arange(T // 256, dtype=I, device="cuda")[None], ints([0]),
+                           dev_status=st)
+    code, s, z = ocache.quantise(v.float().numpy()[0, 0])
+    got = c.vcodes.cpu().numpy().reshape(T, d // 2)
+    assert np.array_equal(np.stack([got & 15, got >> 4], -1).reshape(T, d), code)
+    got = c.vscale.float().cpu().numpy().reshape(T, 2)
+    assert np.array_equal(got[:, 0], s, equal_nan=True) and np.array_equal(got[:, 1], z, equal_nan=True)
+    assert flags(st) == 0
+
+
 def test_append_flags_what_it_cannot_place(cache):
     k = torch.randn(4, 1, 2, 64, device="cuda")
     c = cache.Cache.empty(2, 1, 16, 64)
@@ -289,6 +316,72 @@ def test_kept_sets(cache, d, lens, G, T, N, window, sinks, same):
                 got = out[b, h, t] * kept.size / 15
                 assert np.array_equal(np.rint(got), count)
                 assert np.abs(got - count).max() < 0.01
+
+
+@pytest.mark.parametrize("d,n,G,T,N,window", [
+    (64, 45000, 1, 1, 700, 0),                   # a CTA's slice passes its shared memory
+    (128, 23000, 8, 1, 5000, 0),
+    (64, 46000, 3, 1, 46000, 44000),
+])
+def test_long_contexts(cache, d, n, G, T, N, window):
+    f = Filled(cache, [n, n // 2], 1, d, 256, BF16, seed=n)
+    q, sigma_q = queries(2, G, T, d, BF16)
+    st = status()
+    out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, f.table, ints(f.lens), N,
+                                    0.1, window=window, sinks=5, dev_status=st)
+    assert flags(st) == 0
+    want, bound = f.rows(q, sigma_q, f.lens, [T, T], N, 0.1, window, 5)
+    assert (np.abs(out.cpu().numpy() - want) <= bound).all()
+
+
+@pytest.mark.parametrize("B,H,G,T,d,n,window", [
+    (16, 16, 1, 80, 64, 90, 0), (35, 61, 3, 1, 128, 50, 20), (16, 17, 2, 32, 128, 70, 33),
+    (40, 53, 1, 3, 64, 40, 0)])
+def test_many_short_tiles(cache, B, H, G, T, d, n, window):
+    """More tiles than the card has places for warps."""
+    g = np.random.default_rng(B)
+    lens = [int(x) for x in g.integers(0, n, B)]
+    lens[0] = n
+    f = Filled(cache, lens, H, d, 32, BF16, seed=B)
+    q, sigma_q = queries(B, G * H, T, d, BF16)
+    st = status()
+    out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, f.table, ints(lens), 11, 0.1,
+                                    window=window, sinks=3, dev_status=st).cpu().numpy()
+    assert flags(st) == 0
+    # (every seventh head: the oracle goes row by row)
+    for h in range(0, G * H, 7):
+        sq = np.where(q[:, h].float().numpy() / sigma_q[h].item() < 0, -1, 1)
+        for b in range(B):
+            for t in range(T):
+                o, kept, size = ocache.attend(
+                    sq[b, t], f.sk[b, h // G], f.codes[b, h // G], f.scale[b, h // G],
+                    f.zero[b, h // G], 11, np.float32(0.1), window, 3, lens[b] - T + t)
+                err = np.abs(out[b, h, t] - o)
+                assert (err <= (kept.size / 4 + 64) * 2.0 ** -23 * size).all()
+
+
+def test_pools_beyond_32_bit_offsets(cache):
+    """The last pages of a pool of 5 GB: byte offsets of codes and bits pass 2^32."""
+    page, H, d, n = 256, 8, 128, 700
+    P = 2 ** 32 // (page * H * d // 2) + 300
+    make = lambda *s, dtype: torch.empty(*s, dtype=dtype, device="cuda")      # noqa: E731
+    c = cache.Cache(make(P, H, page, d // 32, dtype=I), make(P, H, page, d // 2, dtype=torch.uint8),
+                    make(P, H, page, 2, dtype=BF16))
+    f = Filled(cache, [n], H, d, page, BF16, seed=1)
+    table = ints([[P - 1, P - 200, P - 7]])
+    st = status()
+    cache.had_cache_append(f.k.cuda(), f.v.cuda(), f.sigma.cuda(), c, table, ints([0]), dev_status=st)
+    got, want = (cache.had_cache_read(x, t, ints([0]), n, dev_status=st)
+                 for x, t in ((c, table), (f.cache, f.table)))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    q, sigma_q = (x.cuda() for x in queries(1, 16, 1, d, BF16))
+    args = ints([n]), 100, 0.1
+    want = cache.had_cache_attention(q, sigma_q, f.cache, f.table, *args, dev_status=st)
+    assert torch.equal(want, cache.had_cache_attention(q, sigma_q, c, table, *args, dev_status=st))
+    cache.had_cache_copy_pages(c, table[0], ints([3, 1, 0]), dev_status=st)
+    assert torch.equal(want, cache.had_cache_attention(q, sigma_q, c, ints([[3, 1, 0]]), *args,
+                                                       dev_status=st))
+    assert flags(st) == 0
 
 
 def test_values_of_any_size_keep_their_weight(cache):
