@@ -108,7 +108,7 @@ had_status_t launch_cluster(void (*kernel)(Params...), size_t smem, cudaStream_t
                            args...);
 }
 
-template <int D, int NA, int W>
+template <int D, int NA, int W, bool kLong>
 had_status_t launch_attention_plan(const had::CacheAttnArgs &a, long long tiles,
                                    had::CacheAttnPlan plan, long long per, cudaStream_t st)
 {
@@ -117,7 +117,7 @@ had_status_t launch_attention_plan(const had::CacheAttnArgs &a, long long tiles,
     plan.by_tiles = had::divisor((unsigned)plan.tiles);
     plan.by_heads = had::divisor((unsigned)a.c.heads);
     plan.by_group = had::divisor((unsigned)(a.Hq / a.c.heads));
-    return launch_clusters(had::cache_attn_kernel<D, NA, W>, (unsigned)(tiles * plan.ctas),
+    return launch_clusters(had::cache_attn_kernel<D, NA, W, kLong>, (unsigned)(tiles * plan.ctas),
                            (unsigned)plan.ctas, 32 * W,
                            had::cache_attn_smem_bytes<D, NA, W>(plan), st, a, plan);
 }
@@ -143,7 +143,7 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStrea
     // them: CTAs of two warps, which wait for one another less (4096 tiles of 8
     // rows and 520 keys: 142 us, with four warps 151 us, with one 200 us).
     if (tiles >= 14 * 148 && keys * key_bytes <= 12 * 1024)
-        return launch_attention_plan<D, NA, 2>(a, tiles, plan, keys, st);
+        return launch_attention_plan<D, NA, 2, false>(a, tiles, plan, keys, st);
     // 20 KB of distances at once, so that four CTAs share an SM
     const long long most = 20 * 1024 / key_bytes / 128 * 128;
     // CTAs until four per SM are busy, each with 512 keys or more, and until a
@@ -156,7 +156,8 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStrea
             (tiles * plan.ctas * 2 <= 4 * 148 && keys > 512LL * plan.ctas)))
         plan.ctas *= 2;
     const long long per = (keys + plan.ctas - 1) / plan.ctas;
-    return launch_attention_plan<D, NA, 4>(a, tiles, plan, per < most ? per : most, st);
+    return per <= most ? launch_attention_plan<D, NA, 4, false>(a, tiles, plan, per, st)
+                       : launch_attention_plan<D, NA, 4, true>(a, tiles, plan, most, st);
 }
 
 template <int D>

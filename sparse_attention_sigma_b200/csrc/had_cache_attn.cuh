@@ -207,7 +207,10 @@ struct CacheAttnShared {
     float zsum[W][RM];
 };
 
-template <int D, int NA, int W>
+// kLong: a CTA's slice may pass `cap` keys, and is then gone through twice, in
+// segments.  A template parameter, since that path costs the other one registers
+// (5 % of the time of 16 k keys a sequence).
+template <int D, int NA, int W, bool kLong>
 __global__ void __launch_bounds__(32 * W, 4 / W * (NA * D <= 64 ? 5 : NA * D <= 128 ? 4 : 2))
 cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 {
@@ -301,7 +304,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     // this CTA's slice of them, whole groups of 32
     const int per = ((total + C - 1) / C + 31) & ~31;
     const int u0 = min(total, rank * per), u1 = min(total, u0 + per);
-    const int segs = max(1, (u1 - u0 + cap - 1) / cap);
+    const int segs = kLong ? max(1, (u1 - u0 + cap - 1) / cap) : 1;
 
     // key u of them: its position; its page's index among the pages of all of them
     const int to_key = lo - first_n, to_page = first_pages - (lo >> lg);
@@ -535,7 +538,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     for (int seg = 0; seg < segs; ++seg) {
         const int s0 = u0 + seg * cap, n = min(cap, u1 - s0);
         const int wb = warp_begin(n, warp), we = warp_begin(n, warp + 1);
-        if (segs > 1) {                       // the slice did not fit: again from the bits
+        if (kLong && segs > 1) {              // the slice did not fit: again from the bits
             __syncthreads();
             load_pages(s0, n);
             __syncthreads();
