@@ -160,12 +160,21 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStrea
                        : launch_attention_plan<D, NA, 4, true>(a, tiles, plan, most, st);
 }
 
+// Tiles of 4 rows; of 8 at d = 64 once those fill four CTAs on every SM.  A tile
+// of 8 unpacks a kept key's codes for twice the rows, but at d = 128 its
+// accumulators halve the warps of an SM, and fewer tiles split a decode's keys
+// less finely.  Measured, 4 rows against 8: d 64, 4 x 512 queries, window 512:
+// 150, 130 us; 4 x 256 dense 96, 77; 16 decodes of 4 k tokens, 8 query heads to
+// a key head 16, 20 us; d 128: 93, 134; 72, 80; 19, 38 us.
 template <int D>
 had_status_t launch_attention(const had::CacheAttnArgs &a, int B, cudaStream_t st)
 {
-    return (long long)(a.Hq / a.c.heads) * a.T <= had::cache_attn_rows(1)
-               ? launch_attention_tile<D, 1>(a, B, st)
-               : launch_attention_tile<D, 2>(a, B, st);
+    if constexpr (D == 64) {
+        const long long rows = (long long)(a.Hq / a.c.heads) * a.T;
+        if (rows > 4 && (rows + 7) / 8 * B * a.c.heads >= 4 * 148)
+            return launch_attention_tile<D, 2>(a, B, st);
+    }
+    return launch_attention_tile<D, 1>(a, B, st);
 }
 
 unsigned grid_for(long long items, int per_block)

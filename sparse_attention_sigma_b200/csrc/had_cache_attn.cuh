@@ -162,7 +162,7 @@ __device__ __forceinline__ int load_of_cta(uint32_t at, int cta)
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
                  "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -211,7 +211,7 @@ struct CacheAttnShared {
 // segments.  A template parameter, since that path costs the other one registers
 // (5 % of the time of 16 k keys a sequence).
 template <int D, int NA, int W, bool kLong>
-__global__ void __launch_bounds__(32 * W, 4 / W * (NA * D <= 64 ? 5 : NA * D <= 128 ? 4 : 2))
+__global__ void __launch_bounds__(32 * W, 4 / W * (NA * D <= 64 && !kLong ? 6 : NA * D <= 64 ? 5 : NA * D <= 128 ? 4 : 2))
 cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 {
     constexpr int kThreads = 32 * W, DW = D / 32;
