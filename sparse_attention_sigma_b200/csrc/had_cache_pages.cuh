@@ -444,10 +444,12 @@ cache_compact_kernel(Books k, int32_t *src, int32_t *dst, int32_t *live_out, int
 }
 
 // Copies pages within a pool, src[i] -> dst[i]; a pair with a negative index
-// is skipped.  HBM-bound: kCopyParts CTAs share a page, each thread moves four
-// 16-byte words of it at once.  A CTA column y takes the pairs y, y + 512, ...;
+// is skipped.  HBM-bound: kCopyParts CTAs share a page, each thread moves up to
+// four 16-byte words of it at once.  A CTA column y takes the pairs y, y + 512, ...;
 // a warp looks at 32 of them with one load each, since most of a list may be
-// empty (1501 pages of 43 KB: 22 us, 19.7 us at 6.6 TB/s).
+// empty (1501 pages of 43 KB, again and again, so that
+// L2 holds part of them: 18 us; 22 us with four words of any array at once and
+// the place of each worked out; 19.7 us at 6.6 TB/s).
 constexpr int kCopyParts = 4;
 
 // 16-byte words of a page in the three arrays.
@@ -460,7 +462,6 @@ cache_copy_kernel(CacheView c, CopyWords words, const int32_t *__restrict__ src,
                   const int32_t *__restrict__ dst, int n, int32_t *status)
 {
     const int lane = threadIdx.x & 31;
-    const long long total = words.codes + words.kbits + words.scale;
     for (int i0 = blockIdx.y; i0 < n; i0 += 32 * gridDim.y) {
         const long long i = i0 + (long long)lane * gridDim.y;
         const int s = i < n ? __ldg(src + i) : -1, d = i < n ? __ldg(dst + i) : -1;
@@ -469,23 +470,29 @@ cache_copy_kernel(CacheView c, CopyWords words, const int32_t *__restrict__ src,
         for (unsigned todo = __ballot_sync(kFullMask, good && s != d); todo; todo &= todo - 1) {
             const int from = __shfl_sync(kFullMask, s, __ffs(todo) - 1);
             const int to = __shfl_sync(kFullMask, d, __ffs(todo) - 1);
-            // word w of a page, the three arrays one behind the other
-            auto place = [&](long long w, int page) -> uint4 * {
-                if (w < words.codes) return reinterpret_cast<uint4 *>(c.vcodes) + page * words.codes + w;
-                w -= words.codes;
-                if (w < words.kbits) return reinterpret_cast<uint4 *>(c.kbits) + page * words.kbits + w;
-                return reinterpret_cast<uint4 *>(c.vscale) + page * words.scale + (w - words.kbits);
-            };
-            constexpr long long kStep = 256 * kCopyParts;
-            for (long long w0 = blockIdx.x * 256 + threadIdx.x; w0 < total; w0 += 4 * kStep) {
-                uint4 x[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (w0 + k * kStep < total) x[k] = *place(w0 + k * kStep, from);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (w0 + k * kStep < total) *place(w0 + k * kStep, to) = x[k];
+            // first words of bits and scales in flight beside those of the codes
+            constexpr int kStep = 256 * kCopyParts;
+            const long long first = blockIdx.x * 256 + threadIdx.x;
+            uint4 *const bits = reinterpret_cast<uint4 *>(c.kbits), *const scale = reinterpret_cast<uint4 *>(c.vscale);
+            const uint4 *const bits_from = bits + from * words.kbits, *const scale_from = scale + from * words.scale;
+            uint4 *const bits_to = bits + to * words.kbits, *const scale_to = scale + to * words.scale;
+            const uint4 *const codes_from = reinterpret_cast<const uint4 *>(c.vcodes) + from * words.codes;
+            uint4 *const codes_to = reinterpret_cast<uint4 *>(c.vcodes) + to * words.codes;
+            uint4 b, z;
+            if (first < words.kbits) b = bits_from[first];
+            if (first < words.scale) z = scale_from[first];
+            for (long long w = first; w < words.codes; w += 2 * kStep) {
+                const bool two = w + kStep < words.codes;
+                const uint4 x = codes_from[w];
+                uint4 y;
+                if (two) y = codes_from[w + kStep];
+                codes_to[w] = x;
+                if (two) codes_to[w + kStep] = y;
             }
+            if (first < words.kbits) bits_to[first] = b;
+            if (first < words.scale) scale_to[first] = z;
+            for (long long w = first + kStep; w < words.kbits; w += kStep) bits_to[w] = bits_from[w];
+            for (long long w = first + kStep; w < words.scale; w += kStep) scale_to[w] = scale_from[w];
         }
     }
 }
