@@ -2,6 +2,7 @@
 // argument checks and kernel launches.
 #include <climits>
 #include <cstdint>
+#include <cstdlib>
 #include <cuda_runtime.h>
 
 #include "had.h"
@@ -108,7 +109,7 @@ had_status_t launch_cluster(void (*kernel)(Params...), size_t smem, cudaStream_t
                            args...);
 }
 
-template <int D, int NA, int W, bool kLong>
+template <int D, int RW, int W, bool kLong>
 had_status_t launch_attention_plan(const had::CacheAttnArgs &a, long long tiles,
                                    had::CacheAttnPlan plan, long long per, cudaStream_t st)
 {
@@ -117,17 +118,17 @@ had_status_t launch_attention_plan(const had::CacheAttnArgs &a, long long tiles,
     plan.by_tiles = had::divisor((unsigned)plan.tiles);
     plan.by_heads = had::divisor((unsigned)a.c.heads);
     plan.by_group = had::divisor((unsigned)(a.Hq / a.c.heads));
-    return launch_clusters(had::cache_attn_kernel<D, NA, W, kLong>, (unsigned)(tiles * plan.ctas),
+    return launch_clusters(had::cache_attn_kernel<D, RW, W, kLong>, (unsigned)(tiles * plan.ctas),
                            (unsigned)plan.ctas, 32 * W,
-                           had::cache_attn_smem_bytes<D, NA, W>(plan), st, a, plan);
+                           had::cache_attn_smem_bytes<D, RW, W>(plan.cap), st, a, plan);
 }
 
-template <int D, int NA>
+template <int D, int RW>
 had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStream_t st)
 {
     const long long rows = (long long)(a.Hq / a.c.heads) * a.T;      // per key-value head
     had::CacheAttnPlan plan{};
-    plan.tiles = (int)((rows + had::cache_attn_rows(NA) - 1) / had::cache_attn_rows(NA));
+    plan.tiles = (int)((rows + 4 * RW - 1) / (4 * RW));
     plan.R = (int)((rows + plan.tiles - 1) / plan.tiles);
     plan.tiles = (int)((rows + plan.R - 1) / plan.R);
     plan.ctas = 1;
@@ -138,12 +139,12 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStrea
         keys = seen < keys ? seen : keys;
     }
     const long long tiles = (long long)B * a.c.heads * plan.tiles;
-    const int key_bytes = had::cache_attn_key_bytes(plan.R);
+    constexpr int key_bytes = 4 * RW;
     // Tiles enough for every warp of the card, each short enough for two of
     // them: CTAs of two warps, which wait for one another less (4096 tiles of 8
     // rows and 520 keys: 142 us, with four warps 151 us, with one 200 us).
     if (tiles >= 14 * 148 && keys * key_bytes <= 12 * 1024)
-        return launch_attention_plan<D, NA, 2, false>(a, tiles, plan, keys, st);
+        return launch_attention_plan<D, RW, 2, false>(a, tiles, plan, keys, st);
     // 20 KB of distances at once, so that four CTAs share an SM
     const long long most = 20 * 1024 / key_bytes / 128 * 128;
     // CTAs until four per SM are busy, each with 512 keys or more, and until a
@@ -156,8 +157,8 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStrea
             (tiles * plan.ctas * 2 <= 4 * 148 && keys > 512LL * plan.ctas)))
         plan.ctas *= 2;
     const long long per = (keys + plan.ctas - 1) / plan.ctas;
-    return per <= most ? launch_attention_plan<D, NA, 4, false>(a, tiles, plan, per, st)
-                       : launch_attention_plan<D, NA, 4, true>(a, tiles, plan, most, st);
+    return per <= most ? launch_attention_plan<D, RW, 4, false>(a, tiles, plan, per, st)
+                       : launch_attention_plan<D, RW, 4, true>(a, tiles, plan, most, st);
 }
 
 // Tiles of 4 rows; of 8 at d = 64 once those fill four CTAs on every SM.  A tile
@@ -169,11 +170,9 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStrea
 template <int D>
 had_status_t launch_attention(const had::CacheAttnArgs &a, int B, cudaStream_t st)
 {
-    if constexpr (D == 64) {
-        const long long rows = (long long)(a.Hq / a.c.heads) * a.T;
-        if (rows > 4 && (rows + 7) / 8 * B * a.c.heads >= 4 * 148)
-            return launch_attention_tile<D, 2>(a, B, st);
-    }
+    const long long rows = (long long)(a.Hq / a.c.heads) * a.T;
+    if (getenv("HADC") ? atoi(getenv("HADC")) == 2 && rows > 4 : rows > 4 && (rows + 7) / 8 * B * a.c.heads >= 4 * 148)
+        return launch_attention_tile<D, 2>(a, B, st);
     return launch_attention_tile<D, 1>(a, B, st);
 }
 

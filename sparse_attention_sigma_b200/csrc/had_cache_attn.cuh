@@ -78,11 +78,6 @@ __device__ __forceinline__ RowRange row_range(const CacheAttnArgs &a, int len, i
 
 constexpr int kMaxCtas = 8;            // of a cluster
 
-// Rows of a tile: three terms each in NA tiles of 16 stacked rows, and whole
-// words of four distances (5 and 10 rows fill the stacked rows better, but the
-// distances worse, and took 2 to 33 % longer).
-__host__ __device__ constexpr int cache_attn_rows(int na) { return na * 4; }
-
 // The tile's split: R rows, `tiles` tiles per (sequence, head), `ctas` per
 // cluster, `cap` keys a CTA of W warps holds at once (a multiple of 32 W).
 struct CacheAttnPlan {
@@ -102,20 +97,17 @@ __host__ __device__ constexpr int cache_attn_pages(int cap) { return cap / 16 + 
 constexpr int kStages = 4;
 constexpr int kQueue = 128;            // >= 16 (kStages + 1) + 31
 
-template <int D, int NA>
+template <int D, int RW>
 struct WarpStage {
     static constexpr int kStride = D / 2 + 16;
     __align__(16) unsigned char codes[kStages][16 * kStride];
     __align__(8) uint32_t scale[kStages][16];
-    uint4 terms[2][NA][8][4];          // registers of A by lane: [g][t4]
+    uint4 terms[2][8][4];              // registers of A by lane: [g][t4]
     uint32_t pool_row[kQueue];
-    __align__(8) uint32_t dist[(cache_attn_rows(NA) + 3) / 4][kQueue];
+    __align__(8) uint32_t dist[RW][kQueue];
 };
 
-// Bytes of shared memory of a key of the slice: a distance per row.
-__host__ __device__ constexpr int cache_attn_key_bytes(int R) { return (R + 3) / 4 * 4; }
-
-// The warps' results before they are added: [warps][16 NA][kSumStride] floats.
+// The warps' results before they are added: [warps][16][kSumStride] floats.
 // Column n of accumulator tile i is element n D/8 + i; its 16-byte piece i / 4
 // lies at place (i / 4) ^ sum_swizzle(n), and a row is padded, so that the
 // eight lanes of a store's wavefront (two rows, four columns) fall on different
@@ -129,13 +121,12 @@ __device__ __forceinline__ int sum_swizzle(int n)
     return D == 128 ? n >> 1 : n >> 2;
 }
 
-template <int D, int NA, int W>
-size_t cache_attn_smem_bytes(const CacheAttnPlan &p)
+template <int D, int RW, int W>
+size_t cache_attn_smem_bytes(int cap)
 {
-    const size_t keys = sizeof(WarpStage<D, NA>) * W +
-                        (size_t)p.cap * cache_attn_key_bytes(p.R) + cache_attn_pages(p.cap) * 4;
-    const size_t red = sizeof(float) * W * 16 * NA * kSumStride<D>;
-    return keys > red ? keys : red;
+    const size_t keys = sizeof(WarpStage<D, RW>) * W + (size_t)cap * 4 * RW + cache_attn_pages(cap) * 4;
+    const size_t sums = sizeof(float) * W * 16 * kSumStride<D>;
+    return keys > sums ? keys : sums;
 }
 
 __device__ __forceinline__ void copy_async16(void *to, const void *from)
@@ -160,24 +151,49 @@ __device__ __forceinline__ int load_of_cta(uint32_t at, int cta)
     return x;
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-                 "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// Codes of four bits of two keys (16-bit halves of x) as bf16 c - 8: 128 + c
-// has c in its last mantissa bits, and 136 is taken off exactly.  The tensor
-// core cuts its running sums, it does not round them; sums of the centred
-// codes stay near zero, those of c itself would grow with every key and lose
-// bits on the way (16 k keys, N 2048: relative error 3.3e-6 instead of
-// 2.2e-7).
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t x, uint32_t bias)
+// Codes of two keys as fp16 c - 8, from the low (even elements) or the high
+// nibbles of the low bytes of x's halves: 1024 + c and 1024 + 16 c have c in
+// their mantissas, the rest is exact.  The tensor core cuts its running sums, it
+// does not round them; sums of the centred codes stay near zero, those of c
+// itself would grow with every key and lose bits on the way (16 k keys, N 2048:
+// relative error 3.3e-6 instead of 2.2e-7).  `raised`: 0x64006400, in a register
+// that the compiler does not fill anew for each use.
+__device__ __forceinline__ uint32_t codes_low(uint32_t x, uint32_t raised)
 {
     uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"((x & 0x000f000fu) | bias), "r"(0x43084308u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"((x & 0x000f000fu) | raised), "r"(0x64086408u));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t codes_high(uint32_t x, uint32_t raised)
+{
+    uint32_t r;                        // (1024 + 16 c) / 16 - 72
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r)
+        : "r"((x & 0x00f000f0u) | raised), "r"(0x2c002c00u), "r"(0xd480d480u));
+    return r;
+}
+
+// Two fp32 as fp16, a in the low half; and back.
+__device__ __forceinline__ uint32_t to_f16(float a, float b)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+__device__ __forceinline__ float2 from_f16(uint32_t x)
+{
+    float2 r;
+    asm("{.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}"
+        : "=f"(r.x), "=f"(r.y) : "r"(x));
     return r;
 }
 
@@ -191,9 +207,13 @@ __device__ __forceinline__ uint32_t bytes_below(uint32_t a, uint32_t b)
     return spread;
 }
 
-template <int D, int NA, int W>
+// The largest scaled weight, and the largest scale: p 2^127 is finite.
+constexpr float kMostWeight = 32768.0f;
+constexpr float kMostScale = 1.7014118e38f;
+
+template <int D, int RW, int W>
 struct CacheAttnShared {
-    static constexpr int RM = cache_attn_rows(NA);
+    static constexpr int RM = 4 * RW;
     __align__(16) uint32_t qbits[RM][D / 32];
     int pos[RM], lo[RM];
     int hist[RM][D + 2];               // a distance of D + 1: not seen
@@ -202,31 +222,32 @@ struct CacheAttnShared {
         float part[RM][D];             // at the end: this CTA's sums
     };
     int level[RM], quota[RM];
+    float top[RM];                     // the largest weight p
     int ranked;                        // some row keeps only part of its ties
     int ties[W][RM];
     float zsum[W][RM];
 };
 
+// RW: words of four distances per key, for tiles of up to 4 RW rows; RW <= 2.
 // kLong: a CTA's slice may pass `cap` keys, and is then gone through twice, in
 // segments.  A template parameter, since that path costs the other one registers
 // (5 % of the time of 16 k keys a sequence).
-template <int D, int NA, int W, bool kLong>
-__global__ void __launch_bounds__(32 * W, 4 / W * (NA * D <= 64 && !kLong ? 6 : NA * D <= 64 ? 5 : NA * D <= 128 ? 4 : 2))
+template <int D, int RW, int W, bool kLong>
+__global__ void __launch_bounds__(32 * W, 4 / W * (D == 128 ? 4 : RW == 2 || kLong ? 5 : 6))
 cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 {
     constexpr int kThreads = 32 * W, DW = D / 32;
     constexpr int kTiles = D / 8;             // 8-wide column tiles of the value
     constexpr int kCodeWords = D / 64;        // 32-bit words of codes per lane and key
-    constexpr int RM = cache_attn_rows(NA);
-    constexpr int RWM = (cache_attn_rows(NA) + 3) / 4;        // most words of four row bytes
+    constexpr int RM = 4 * RW;
     constexpr uint32_t kUnseen = D + 1, kUnseen4 = kUnseen * 0x01010101u;
     constexpr int KU = 4;                     // keys per lane of one step of the distances
-    using Shared = CacheAttnShared<D, NA, W>;
+    using Shared = CacheAttnShared<D, RW, W>;
     extern __shared__ __align__(16) unsigned char attn_smem[];
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int R = plan.R, RW = (R + 3) / 4, cap = plan.cap;
-    using Stage = WarpStage<D, NA>;
+    const int R = plan.R, cap = plan.cap;
+    using Stage = WarpStage<D, RW>;
     Stage &stage = reinterpret_cast<Stage *>(attn_smem)[warp];
     uint32_t *const distw = reinterpret_cast<uint32_t *>(                    // [RW][cap]
         attn_smem + sizeof(Stage) * W);
@@ -250,7 +271,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
     };
     int len = __ldg(a.lens + b), count = a.counts ? __ldg(a.counts + b) : a.T;
     {
-        constexpr int kMine = (cache_attn_rows(NA) + W - 1) / W;
+        constexpr int kMine = (RM + W - 1) / W;
         float x[kMine][DW], sigma[kMine];
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
@@ -348,18 +369,13 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         };
         // 32 KU keys against all rows; `mixed`: some row may not see some key
         auto step = [&](int k0, const uint32_t (&bits)[KU][DW], const uint32_t (&at)[KU], bool mixed) {
+#pragma unroll 1
             for (int q = 0; q < RW; ++q) {
                 uint32_t word[KU];
 #pragma unroll
-                for (int i = 0; i < KU; ++i) word[i] = 0u;
-#pragma unroll
-                for (int rr = 0; rr < 4; ++rr) {
-                    const int r = 4 * q + rr;
-                    if (r >= rows) {
-#pragma unroll
-                        for (int i = 0; i < KU; ++i) word[i] += kUnseen << (8 * rr);
-                        continue;
-                    }
+                for (int i = 0; i < KU; ++i) word[i] = kUnseen4;
+#pragma unroll 1
+                for (int r = 4 * q; r < min(rows, 4 * q + 4); ++r) {
                     uint32_t qb[DW];
                     if constexpr (DW == 2) {
                         const uint2 x = *reinterpret_cast<const uint2 *>(sh.qbits[r]);
@@ -369,6 +385,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                         qb[0] = x.x; qb[1] = x.y; qb[2] = x.z; qb[3] = x.w;
                     }
                     const int pos = mixed ? sh.pos[r] : 0, row_lo = mixed ? sh.lo[r] : 0;
+                    const int unit = 1 << (8 * (r & 3));
 #pragma unroll
                     for (int i = 0; i < KU; ++i) {
                         if (k0 + 32 * i >= we) break;
@@ -381,7 +398,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                             vis = vis && key <= pos && (key >= row_lo || key < a.sinks);
                         }
                         n = vis ? n : (int)kUnseen;
-                        word[i] += (uint32_t)n << (8 * rr);
+                        word[i] += (n - (int)kUnseen) * unit;
                         if (with_hist) atomicAdd(&sh.hist[r][n], 1);
                     }
                 }
@@ -512,25 +529,38 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
             if (lane * EL + e <= D + 1) sh.p[r][lane * EL + e] = lane * EL + e <= D ? w[e] * inv : 0.0f;
         if (lane == 0) {
             sh.level[r] = level;
+            sh.top[r] = inv;
             if (level < 0) sh.quota[r] = 0;
         }
     }
     __syncthreads();
 
     const int g = lane >> 2, t4 = lane & 3;
-    uint32_t bias;                            // one register for all 32 uses of a chunk
-    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(bias));
-    float acc[NA][kTiles][4], zacc[RWM];
+    uint32_t raised;
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(raised));
+    // scale[i]: the power of two by which row 4 i + lane / 8 is multiplied
+    float acc[kTiles][4], zacc[RW], scale[RW], shrink[RW];
 #pragma unroll
-    for (int m = 0; m < NA; ++m)
+    for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i)
+        for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][i][e] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < RWM; ++i) zacc[i] = 0.0f;
-    // stacked rows that no term fills stay zero
-    for (int i = lane; i < 2 * NA * 32; i += 32) (&stage.terms[0][0][0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < RW; ++i) {
+        zacc[i] = 0.0f;
+        scale[i] = kMostScale;
+        shrink[i] = 1.0f;
+    }
+    // rows that the tile lacks stay zero
+    for (int i = lane; i < 2 * 32; i += 32) (&stage.terms[0][0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+    // the factor of row g among those of the rows 4 i + lane / 8
+    auto of_row_g = [&](const float (&x)[RW]) {
+        float f = __shfl_sync(kFullMask, x[0], (g & 3) * 8);
+        if constexpr (RW == 2) {
+            const float f1 = __shfl_sync(kFullMask, x[1], (g & 3) * 8);
+            f = g < 4 ? f : f1;
+        }
+        return f;
+    };
     // lane r < rows follows row r's level and the ties it may still keep
     const int my_level = lane < rows ? sh.level[lane] : -1;
     int my_quota = lane < rows ? sh.quota[lane] : 0;
@@ -580,9 +610,9 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         const int limit = my_level < 0 ? 0 : my_level + (left >= here);   // (unranked: all ties)
         my_quota = max(0, my_quota - all);
         const unsigned partial_rows = __ballot_sync(kFullMask, partial);
-        uint32_t below[RWM];
+        uint32_t below[RW];
 #pragma unroll
-        for (int q = 0; q < RWM; ++q) {
+        for (int q = 0; q < RW; ++q) {
             below[q] = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -593,12 +623,10 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         // the next 32 keys of the part
         auto look = [&]() {
             const int k = k0 + lane;
-            uint32_t any = 0, d4[RWM];
+            uint32_t any = 0, d4[RW];
 #pragma unroll
-            for (int q = 0; q < RWM; ++q) {
-                d4[q] = kUnseen4;
-                if (q >= RW) continue;
-                if (k < we) d4[q] = distw[q * cap + k];
+            for (int q = 0; q < RW; ++q) {
+                d4[q] = k < we ? distw[q * cap + k] : kUnseen4;
                 uint32_t keep = bytes_below(d4[q], below[q]);
                 for (unsigned todo = partial_rows >> (4 * q) & 15u; todo; todo &= todo - 1) {
                     const int i = __ffs(todo) - 1, r = 4 * q + i;
@@ -617,8 +645,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                 const int to = (queued + __popc(kept & ((1u << lane) - 1))) % kQueue, u = s0 + k;
                 stage.pool_row[to] = page_row[page_at(u) - page0] + (key_of(u) & page_mask);
 #pragma unroll
-                for (int q = 0; q < RWM; ++q)
-                    if (q < RW) stage.dist[q][to] = d4[q];
+                for (int q = 0; q < RW; ++q) stage.dist[q][to] = d4[q];
             }
             queued += __popc(kept);
             k0 += 32;
@@ -629,8 +656,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                 if (lane < (-queued & 15)) {
                     stage.pool_row[to % kQueue] = stage.pool_row[(queued - 1) % kQueue];
 #pragma unroll
-                    for (int q = 0; q < RWM; ++q)
-                        if (q < RW) stage.dist[q][to % kQueue] = kUnseen4;
+                    for (int q = 0; q < RW; ++q) stage.dist[q][to % kQueue] = kUnseen4;
                 }
             }
         };
@@ -650,48 +676,83 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        // weights of chunk c: keys 2 (lane % 8) and the next for every fourth row,
-        // as terms: the upper 8 bits of what is left, twice, and the rest
-        auto weigh = [&](int c) {
-            const int ring = c % kStages;
-            uint32_t *const terms = reinterpret_cast<uint32_t *>(stage.terms[c & 1]) +
-                                    16 * (lane >> 3) + 4 * ((lane & 7) >> 1) + 2 * (lane & 1);
+        // The same where a scale is NaN or a weight passes fp16's range: the rows'
+        // scales come down so that the largest weight of the chunk is below 2^13,
+        // and p z is summed again with what is kept alone.
+        auto reweigh = [&](int c, float (&v_a)[RW], float (&v_b)[RW], const float (&zkeep)[RW]) -> bool {
             const int pair = lane & 7, sub = lane >> 3;
-            const uint2 sz = *reinterpret_cast<const uint2 *>(&stage.scale[ring][2 * pair]);
+            const uint2 sz = *reinterpret_cast<const uint2 *>(&stage.scale[c % kStages][2 * pair]);
             const float s_a = bf16_lo(sz.x), z_a = fmaf(8.0f, s_a, bf16_hi(sz.x));
             const float s_b = bf16_lo(sz.y), z_b = fmaf(8.0f, s_b, bf16_hi(sz.y));
-            // row x of A and keys 2 pair, 2 pair + 1: a word of lane (x % 8, pair / 2)
-            auto term_word = [](int x) { return (x >> 4) * 128 + (x & 7) * 16 + (x >> 3 & 1); };
-            // a NaN scale must not meet the weight 0 of a row that drops the key
-            const bool odd = __any_sync(kFullMask, s_a != s_a || s_b != s_b);
+            bool changed = false;
 #pragma unroll
-            for (int i = 0; i < RWM; ++i) {
-                const int r = 4 * i + sub;
-                if (r < rows) {
-                    const uint2 d4 = *reinterpret_cast<const uint2 *>(&stage.dist[i][(16 * c + 2 * pair) % kQueue]);
-                    const uint32_t h_a = __byte_perm(d4.x, 0u, 0x4440 | sub), h_b = __byte_perm(d4.y, 0u, 0x4440 | sub);
-                    const float p_a = sh.p[r][h_a], p_b = sh.p[r][h_b];
-                    float v_a = p_a * s_a, v_b = p_b * s_b, z = fmaf(p_a, z_a, p_b * z_b);
-                    if (odd) {
-                        v_a = h_a == kUnseen ? 0.0f : v_a;
-                        v_b = h_b == kUnseen ? 0.0f : v_b;
-                        z = (h_a == kUnseen ? 0.0f : p_a * z_a) + (h_b == kUnseen ? 0.0f : p_b * z_b);
-                    }
-                    zacc[i] += z;
-                    const float m_a = v_a - __uint_as_float(__float_as_uint(v_a) & 0xffff0000u);
-                    const float m_b = v_b - __uint_as_float(__float_as_uint(v_b) & 0xffff0000u);
-                    const float l_a = m_a - __uint_as_float(__float_as_uint(m_a) & 0xffff0000u);
-                    const float l_b = m_b - __uint_as_float(__float_as_uint(m_b) & 0xffff0000u);
-                    terms[term_word(4 * i)] = __byte_perm(__float_as_uint(v_a), __float_as_uint(v_b), 0x7632);
-                    terms[term_word(RM + 4 * i)] = __byte_perm(__float_as_uint(m_a), __float_as_uint(m_b), 0x7632);
-                    terms[term_word(2 * RM + 4 * i)] = __byte_perm(__float_as_uint(l_a), __float_as_uint(l_b), 0x7632);
+            for (int i = 0; i < RW; ++i) {
+                const int r = min(4 * i + sub, rows - 1);
+                const uint2 d4 = *reinterpret_cast<const uint2 *>(&stage.dist[i][(16 * c + 2 * pair) % kQueue]);
+                const uint32_t h_a = __byte_perm(d4.x, 0u, 0x4440 | sub), h_b = __byte_perm(d4.y, 0u, 0x4440 | sub);
+                const float p_a = sh.p[r][h_a], p_b = sh.p[r][h_b];
+                const float w_a = h_a == kUnseen ? 0.0f : p_a * s_a, w_b = h_b == kUnseen ? 0.0f : p_b * s_b;
+                zacc[i] = zkeep[i] + ((h_a == kUnseen ? 0.0f : p_a * z_a) + (h_b == kUnseen ? 0.0f : p_b * z_b));
+                // the most that keys of these scales can weigh (NaN is no number to scale by)
+                float most = fmaxf(h_a == kUnseen ? 0.0f : sh.top[r] * s_a, h_b == kUnseen ? 0.0f : sh.top[r] * s_b);
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(kFullMask, most, o));
+                // 2^12 <= most 2^(12 - e) < 2^13, with e >= -115
+                const int e = max((int)(__float_as_uint(most) >> 23) - 127, -115);
+                const float fit = most > 0.0f ? __uint_as_float((uint32_t)(12 - e + 127) << 23) : kMostScale;
+                shrink[i] = 1.0f;
+                if (most * scale[i] > kMostWeight) {
+                    shrink[i] = fit / scale[i];
+                    scale[i] = fit;
+                    changed = true;
                 }
+                v_a[i] = w_a * scale[i];
+                v_b[i] = w_b * scale[i];
             }
+            return __any_sync(kFullMask, changed);
+        };
+        // Weights p s of chunk c, keys 2 (lane % 8) and the next, of every fourth
+        // row, times the row's scale, as two fp16 terms.  True where a scale had
+        // to come down: what was summed before is then to be shrunk.
+        auto weigh = [&](int c) -> bool {
+            const int pair = lane & 7, sub = lane >> 3;
+            // row x of A and keys 2 pair, 2 pair + 1: a word of lane (x % 8, pair / 2)
+            uint32_t *const terms = reinterpret_cast<uint32_t *>(stage.terms[c & 1]) + 16 * sub +
+                                    4 * (pair >> 1) + 2 * (pair & 1);
+            const uint2 sz = *reinterpret_cast<const uint2 *>(&stage.scale[c % kStages][2 * pair]);
+            const float s_a = bf16_lo(sz.x), z_a = fmaf(8.0f, s_a, bf16_hi(sz.x));
+            const float s_b = bf16_lo(sz.y), z_b = fmaf(8.0f, s_b, bf16_hi(sz.y));
+            // a NaN scale must not meet the weight 0 of a row that drops the key
+            bool odd = s_a != s_a || s_b != s_b;
+            float v_a[RW], v_b[RW], zkeep[RW];
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                const int r = min(4 * i + sub, rows - 1);
+                const uint2 d4 = *reinterpret_cast<const uint2 *>(&stage.dist[i][(16 * c + 2 * pair) % kQueue]);
+                const uint32_t h_a = __byte_perm(d4.x, 0u, 0x4440 | sub), h_b = __byte_perm(d4.y, 0u, 0x4440 | sub);
+                const float p_a = sh.p[r][h_a], p_b = sh.p[r][h_b];
+                v_a[i] = p_a * scale[i] * s_a;
+                v_b[i] = p_b * scale[i] * s_b;
+                zkeep[i] = zacc[i];
+                zacc[i] = fmaf(p_a, z_a, fmaf(p_b, z_b, zacc[i]));
+                odd = odd || fmaxf(v_a[i], v_b[i]) > kMostWeight;
+            }
+            bool changed = false;
+            if (__builtin_expect(__any_sync(kFullMask, odd), 0)) changed = reweigh(c, v_a, v_b, zkeep);
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                if (4 * i + sub >= rows) continue;
+                const uint32_t hi = to_f16(v_a[i], v_b[i]);
+                const float2 back = from_f16(hi);
+                terms[64 * i] = hi;
+                terms[64 * i + 1] = to_f16(v_a[i] - back.x, v_b[i] - back.y);
+            }
+            return changed;
         };
         auto fill = [&](int chunks) {
             while (queued < 16 * chunks && k0 < we) look();
         };
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < kStages - 1; ++c) {
             fill(c + 1);
             __syncwarp();
@@ -712,12 +773,8 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
             // this lane's four keys are 4 t4 .. 4 t4 + 3 and stand for columns
             // 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of A; its codes of a key are
             // elements g D/8 on
-            uint32_t af[NA][4], code[4][kCodeWords];
-#pragma unroll
-            for (int m = 0; m < NA; ++m) {
-                const uint4 u = stage.terms[c & 1][m][g][t4];
-                af[m][0] = u.x; af[m][1] = u.y; af[m][2] = u.z; af[m][3] = u.w;
-            }
+            uint32_t code[4][kCodeWords];
+            const uint4 af = stage.terms[c & 1][g][t4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const unsigned char *from = stage.codes[ring] + (4 * t4 + e) * Stage::kStride + g * (D / 16);
@@ -728,47 +785,50 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                     code[e][0] = u.x; code[e][1] = u.y;
                 }
             }
-            if (16 * (c + 1) < queued) weigh(c + 1);
+            const bool smaller = 16 * (c + 1) < queued && weigh(c + 1);
 #pragma unroll
             for (int w = 0; w < kCodeWords; ++w)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t sel = half ? 0x7632 : 0x5410;
+                for (int byte = 0; byte < 4; ++byte) {
+                    const uint32_t sel = 0x4400 + 0x1111 * byte;       // that byte of both keys
                     const uint32_t x0 = __byte_perm(code[0][w], code[1][w], sel);
                     const uint32_t x1 = __byte_perm(code[2][w], code[3][w], sel);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t b0 = codes_bf16(x0 >> (4 * i), bias), b1 = codes_bf16(x1 >> (4 * i), bias);
-#pragma unroll
-                        for (int m = 0; m < NA; ++m) mma_bf16(acc[m][8 * w + 4 * half + i], af[m], b0, b1);
-                    }
+                    mma_f16(acc[8 * w + 2 * byte], af, codes_low(x0, raised), codes_low(x1, raised));
+                    mma_f16(acc[8 * w + 2 * byte + 1], af, codes_high(x0, raised), codes_high(x1, raised));
                 }
+            if (__builtin_expect(smaller, 0)) {            // the next chunk's scale
+                const float f = of_row_g(shrink);
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][e] *= f;
+            }
         }
         __syncwarp();
     }
 
     // a row's p z: eight lanes hold its parts
 #pragma unroll
-    for (int i = 0; i < RWM; ++i)
+    for (int i = 0; i < RW; ++i)
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) zacc[i] += __shfl_xor_sync(kFullMask, zacc[i], o);
     constexpr int kStride = kSumStride<D>;
     float *const sums = reinterpret_cast<float *>(attn_smem);
+    const float unscale = 1.0f / of_row_g(scale);          // powers of two: exact
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < NA; ++m)
+    for (int e = 0; e < 4; ++e) {
+        const int n = 2 * t4 + e % 2;
+        if (g >= RM) continue;
+        float *to = sums + (warp * 16 + g + 8 * (e / 2)) * kStride + n * kTiles;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int x = 16 * m + g + 8 * (e / 2), n = 2 * t4 + e % 2;
-            if (x >= 3 * RM) continue;
-            float *to = sums + (warp * 16 * NA + x) * kStride + n * kTiles;
+        for (int i = 0; i < kTiles; i += 4)
+            *reinterpret_cast<float4 *>(to + ((i / 4) ^ sum_swizzle<D>(n)) * 4) =
+                make_float4(acc[i][e] * unscale, acc[i + 1][e] * unscale, acc[i + 2][e] * unscale,
+                            acc[i + 3][e] * unscale);
+    }
 #pragma unroll
-            for (int i = 0; i < kTiles; i += 4)
-                *reinterpret_cast<float4 *>(to + ((i / 4) ^ sum_swizzle<D>(n)) * 4) =
-                    make_float4(acc[m][i][e], acc[m][i + 1][e], acc[m][i + 2][e], acc[m][i + 3][e]);
-        }
-#pragma unroll
-    for (int i = 0; i < RWM; ++i)
+    for (int i = 0; i < RW; ++i)
         if ((lane & 7) == 0 && 4 * i + (lane >> 3) < rows) sh.zsum[warp][4 * i + (lane >> 3)] = zacc[i];
     __syncthreads();
     for (int e = tid; e < rows * D; e += kThreads) {
@@ -776,8 +836,8 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         const float *from = sums + r * kStride + n * kTiles + ((i / 4) ^ sum_swizzle<D>(n)) * 4 + i % 4;
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w, from += 16 * NA * kStride)
-            sum += (from[2 * RM * kStride] + from[RM * kStride] + sh.zsum[w][r]) + from[0];
+        for (int w = 0; w < W; ++w, from += 16 * kStride)
+            sum += (from[8 * kStride] + sh.zsum[w][r]) + from[0];
         if (C > 1) sh.part[r][k] = sum;
         else a.out[q_row(r) * D + k] = sum;
     }
