@@ -2,7 +2,6 @@
 // argument checks and kernel launches.
 #include <climits>
 #include <cstdint>
-#include <cstdlib>
 #include <cuda_runtime.h>
 
 #include "had.h"
@@ -109,18 +108,19 @@ had_status_t launch_cluster(void (*kernel)(Params...), size_t smem, cudaStream_t
                            args...);
 }
 
-template <int D, int RW, int W, bool kLong>
+template <int D, int RW, bool kLong>
 had_status_t launch_attention_plan(const had::CacheAttnArgs &a, long long tiles,
                                    had::CacheAttnPlan plan, long long per, cudaStream_t st)
 {
-    plan.cap = (int)((per + 32 * W - 1) / (32 * W) * (32 * W));
+    constexpr int kThreads = had::kCacheAttnThreads;
+    plan.cap = (int)((per + kThreads - 1) / kThreads * kThreads);
     if (tiles * plan.ctas > INT_MAX) return HAD_ERR_UNSUPPORTED;
     plan.by_tiles = had::divisor((unsigned)plan.tiles);
     plan.by_heads = had::divisor((unsigned)a.c.heads);
     plan.by_group = had::divisor((unsigned)(a.Hq / a.c.heads));
-    return launch_clusters(had::cache_attn_kernel<D, RW, W, kLong>, (unsigned)(tiles * plan.ctas),
-                           (unsigned)plan.ctas, 32 * W,
-                           had::cache_attn_smem_bytes<D, RW, W>(plan.cap), st, a, plan);
+    return launch_clusters(had::cache_attn_kernel<D, RW, kLong>, (unsigned)(tiles * plan.ctas),
+                           (unsigned)plan.ctas, kThreads,
+                           had::cache_attn_smem_bytes<D, RW>(plan.cap), st, a, plan);
 }
 
 template <int D, int RW>
@@ -139,14 +139,8 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStrea
         keys = seen < keys ? seen : keys;
     }
     const long long tiles = (long long)B * a.c.heads * plan.tiles;
-    constexpr int key_bytes = 4 * RW;
-    // Tiles enough for every warp of the card, each short enough for two of
-    // them: CTAs of two warps, which wait for one another less (4096 tiles of 8
-    // rows and 520 keys: 142 us, with four warps 151 us, with one 200 us).
-    if (tiles >= 14 * 148 && keys * key_bytes <= 12 * 1024)
-        return launch_attention_plan<D, RW, 2, false>(a, tiles, plan, keys, st);
     // 20 KB of distances at once, so that four CTAs share an SM
-    const long long most = 20 * 1024 / key_bytes / 128 * 128;
+    constexpr long long most = 20 * 1024 / (4 * RW) / 128 * 128;
     // CTAs until four per SM are busy, each with 512 keys or more, and until a
     // CTA holds its slice whole (a longer one is gone through twice).  Measured
     // with 1, 2, 4 and 8: 64 tiles of 4 k keys 39, 24, 15.7, 15.0 us; 128 of
@@ -157,21 +151,21 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStrea
             (tiles * plan.ctas * 2 <= 4 * 148 && keys > 512LL * plan.ctas)))
         plan.ctas *= 2;
     const long long per = (keys + plan.ctas - 1) / plan.ctas;
-    return per <= most ? launch_attention_plan<D, RW, 4, false>(a, tiles, plan, per, st)
-                       : launch_attention_plan<D, RW, 4, true>(a, tiles, plan, most, st);
+    return per <= most ? launch_attention_plan<D, RW, false>(a, tiles, plan, per, st)
+                       : launch_attention_plan<D, RW, true>(a, tiles, plan, most, st);
 }
 
-// Tiles of 4 rows; of 8 at d = 64 once those fill four CTAs on every SM.  A tile
-// of 8 unpacks a kept key's codes for twice the rows, but at d = 128 its
-// accumulators halve the warps of an SM, and fewer tiles split a decode's keys
-// less finely.  Measured, 4 rows against 8: d 64, 4 x 512 queries, window 512:
-// 150, 130 us; 4 x 256 dense 96, 77; 16 decodes of 4 k tokens, 8 query heads to
-// a key head 16, 20 us; d 128: 93, 134; 72, 80; 19, 38 us.
+// Tiles of 8 rows once clusters of four CTAs on them put three on every SM, of 4
+// rows else.  A tile of 8 unpacks a kept key's codes for twice the rows, but
+// fewer tiles split a decode's keys less finely.  Measured, 4 rows against 8, d 64:
+// 4 x 512 queries under a window of 512 150, 125 us; 4 x 256 dense ones 100,
+// 68; 16 decodes of 4 k tokens, 8 query heads to a key head, 16.8, 20 us;
+// d 128: 91, 89; 74, 55; 20, 27 us.
 template <int D>
 had_status_t launch_attention(const had::CacheAttnArgs &a, int B, cudaStream_t st)
 {
     const long long rows = (long long)(a.Hq / a.c.heads) * a.T;
-    if (getenv("HADC") ? atoi(getenv("HADC")) == 2 && rows > 4 : rows > 4 && (rows + 7) / 8 * B * a.c.heads >= 4 * 148)
+    if (rows > 4 && (rows + 7) / 8 * B * a.c.heads * 4 >= 3 * 148)
         return launch_attention_tile<D, 2>(a, B, st);
     return launch_attention_tile<D, 1>(a, B, st);
 }

@@ -13,7 +13,7 @@
 //
 // One cluster of CTAs takes a tile of R rows that share a key-value head (its
 // query heads, and neighbouring tokens of a draft or chunk) and splits the keys
-// that any of them sees; a CTA's warps split its slice, in key order.
+// that any of them sees; a CTA's four warps split its slice, in key order.
 //   1. Distances: a lane per key, the key's bits in registers, XOR + popc with
 //      every row's bits from shared memory; 8-bit distances stay in shared
 //      memory (d + 1: not visible), counts go to the CTA's histograms.
@@ -24,23 +24,28 @@
 //      (ties by rank in key order) and queues the keys that at least one row
 //      keeps; their codes and scales are copied to shared memory from there.
 //   4. Per 16 queued keys, behind their copies: the tile's P V on the tensor
-//      core.  The codes are whole numbers below 16, exact in bf16; the weights
-//      p s are fp32 and are cut into three bf16 terms, which hold all 24 bits,
-//      and stacked as rows of A: row x = 4 NA term + r.  So the product is as
-//      exact as fp32 and any scale keeps its exponent.  The product takes c - 8
-//      in place of c; the rest, p (z + 8 s), is summed beside it.
+//      core.  The codes are whole numbers below 16, exact in fp16; the weights
+//      p s are fp32, brought into fp16's range by a power of two per row that
+//      only comes down when a larger weight appears, and cut into two fp16
+//      terms (24 bits, down to 2^-36 of the row's largest weight), stacked as
+//      rows of A: row x = 8 term + r.  So the product is as exact as fp32 for
+//      scales of any size.  It takes c - 8 in place of c; the rest, p (z + 8 s),
+//      is summed beside it.
 //   5. Warps, terms and CTAs are added in a fixed order.
 // The union of the rows' kept keys is read once, each key's bits once.
 //
 // mma.sync and not tcgen05: a tile has 4 or 8 rows of 64 or 128, B is made in
-// registers from gathered codes, and the tensor pipe is 8 % busy.  What bounds
+// registers from gathered codes, and the tensor pipe is 10 % busy.  What bounds
 // it is the issue of the instructions around the product (16 sequences of 16 k
-// tokens, 32 query and 8 key heads, d 128, N 2048: 72 us, 34 M warp
+// tokens, 32 query and 8 key heads, d 128, N 2048: 68 us, 31 M warp
 // instructions, half of all issue slots; 127 MB from memory would take 19 us):
-// about 20 a (row, 32 keys) for distances and selection, 350 per 16 kept keys
-// of d 128, of which 128 unpack and multiply codes, 80 make the weights and 45
-// copy.  16 warps an SM is what the accumulators' registers allow; 20 and 24
-// warps spill (95 and 115 us), 12 hide less (92 us).
+// about 20 a (row, 32 keys) for distances and selection, 300 per 16 kept keys
+// of d 128, of which 100 unpack and multiply codes, 70 make the weights and 40
+// copy.  The accumulators' registers allow 16 warps an SM at d 128 and 20 to 24
+// at 64; more spill (20 and 24 at d 128, with the bf16 form of step 4: 95 and
+// 115 us against 72), fewer hide less (12: 92 us).  Loops over rows and over
+// the first copies are kept rolled: unrolled, the kernel passes what the SM
+// holds of instructions (windowed chunks 141 against 125 us).
 #pragma once
 #include <cooperative_groups.h>
 
@@ -77,9 +82,10 @@ __device__ __forceinline__ RowRange row_range(const CacheAttnArgs &a, int len, i
 }
 
 constexpr int kMaxCtas = 8;            // of a cluster
+constexpr int kCacheAttnThreads = 128, kCacheAttnWarps = kCacheAttnThreads / 32;
 
 // The tile's split: R rows, `tiles` tiles per (sequence, head), `ctas` per
-// cluster, `cap` keys a CTA of W warps holds at once (a multiple of 32 W).
+// cluster, `cap` keys a CTA holds at once (a multiple of its threads).
 struct CacheAttnPlan {
     int R, tiles, ctas, cap;
     Divisor by_tiles, by_heads, by_group;      // of tiles, heads, query heads per head
@@ -121,11 +127,11 @@ __device__ __forceinline__ int sum_swizzle(int n)
     return D == 128 ? n >> 1 : n >> 2;
 }
 
-template <int D, int RW, int W>
+template <int D, int RW>
 size_t cache_attn_smem_bytes(int cap)
 {
-    const size_t keys = sizeof(WarpStage<D, RW>) * W + (size_t)cap * 4 * RW + cache_attn_pages(cap) * 4;
-    const size_t sums = sizeof(float) * W * 16 * kSumStride<D>;
+    const size_t keys = sizeof(WarpStage<D, RW>) * kCacheAttnWarps + (size_t)cap * 4 * RW + cache_attn_pages(cap) * 4;
+    const size_t sums = sizeof(float) * kCacheAttnWarps * 16 * kSumStride<D>;
     return keys > sums ? keys : sums;
 }
 
@@ -211,7 +217,7 @@ __device__ __forceinline__ uint32_t bytes_below(uint32_t a, uint32_t b)
 constexpr float kMostWeight = 32768.0f;
 constexpr float kMostScale = 1.7014118e38f;
 
-template <int D, int RW, int W>
+template <int D, int RW>
 struct CacheAttnShared {
     static constexpr int RM = 4 * RW;
     __align__(16) uint32_t qbits[RM][D / 32];
@@ -224,25 +230,25 @@ struct CacheAttnShared {
     int level[RM], quota[RM];
     float top[RM];                     // the largest weight p
     int ranked;                        // some row keeps only part of its ties
-    int ties[W][RM];
-    float zsum[W][RM];
+    int ties[kCacheAttnWarps][RM];
+    float zsum[kCacheAttnWarps][RM];
 };
 
 // RW: words of four distances per key, for tiles of up to 4 RW rows; RW <= 2.
 // kLong: a CTA's slice may pass `cap` keys, and is then gone through twice, in
 // segments.  A template parameter, since that path costs the other one registers
 // (5 % of the time of 16 k keys a sequence).
-template <int D, int RW, int W, bool kLong>
-__global__ void __launch_bounds__(32 * W, 4 / W * (D == 128 ? 4 : RW == 2 || kLong ? 5 : 6))
+template <int D, int RW, bool kLong>
+__global__ void __launch_bounds__(kCacheAttnThreads, D == 128 ? 4 : RW == 2 || kLong ? 5 : 6)
 cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
 {
-    constexpr int kThreads = 32 * W, DW = D / 32;
+    constexpr int kThreads = kCacheAttnThreads, W = kCacheAttnWarps, DW = D / 32;
     constexpr int kTiles = D / 8;             // 8-wide column tiles of the value
     constexpr int kCodeWords = D / 64;        // 32-bit words of codes per lane and key
     constexpr int RM = 4 * RW;
     constexpr uint32_t kUnseen = D + 1, kUnseen4 = kUnseen * 0x01010101u;
     constexpr int KU = 4;                     // keys per lane of one step of the distances
-    using Shared = CacheAttnShared<D, RW, W>;
+    using Shared = CacheAttnShared<D, RW>;
     extern __shared__ __align__(16) unsigned char attn_smem[];
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
