@@ -106,8 +106,12 @@ constexpr int kQueue = 128;            // >= 16 (kStages + 1) + 31
 template <int D, int RW>
 struct WarpStage {
     static constexpr int kStride = D / 2 + 16;
-    __align__(16) unsigned char codes[kStages][16 * kStride];
+    union {
+        __align__(16) unsigned char codes[kStages][16 * kStride];
+        int hist[4 * RW][D + 2];       // before: this warp's counts; D + 1: not seen
+    };
     __align__(8) uint32_t scale[kStages][16];
+    // (these three also hold a row's counts on their way from the cluster)
     uint4 terms[2][8][4];              // registers of A by lane: [g][t4]
     uint32_t pool_row[kQueue];
     __align__(8) uint32_t dist[RW][kQueue];
@@ -222,7 +226,7 @@ struct CacheAttnShared {
     static constexpr int RM = 4 * RW;
     __align__(16) uint32_t qbits[RM][D / 32];
     int pos[RM], lo[RM];
-    int hist[RM][D + 2];               // a distance of D + 1: not seen
+    int hist[RM][D + 2];               // the counts of all warps
     union {
         float p[RM][D + 2];            // weight of a distance; 0 for D + 1
         float part[RM][D];             // at the end: this CTA's sums
@@ -303,7 +307,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         }
         if (tid == 0) sh.ranked = 0;
     }
-    for (int i = tid; i < R * (D + 2); i += kThreads) (&sh.hist[0][0])[i] = 0;
+    for (int i = lane; i < RM * (D + 2); i += 32) (&stage.hist[0][0])[i] = 0;
     if (len < 0 || len > (long long)a.max_pages << lg || count < 0 || count > a.T) {
         if (tid == 0) flag(a.status, HAD_ERR_INVALID_ARG);
         len = count = 0;
@@ -405,7 +409,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                         }
                         n = vis ? n : (int)kUnseen;
                         word[i] += (n - (int)kUnseen) * unit;
-                        if (with_hist) atomicAdd(&sh.hist[r][n], 1);
+                        if (with_hist) atomicAdd(&stage.hist[r][n], 1);
                     }
                 }
 #pragma unroll
@@ -442,6 +446,13 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         __syncthreads();
         distances(s0, warp_begin(n, warp), warp_begin(n, warp + 1), true);
     }
+    __syncthreads();
+    for (int i = tid; i < rows * (D + 2); i += kThreads) {
+        int n = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) n += (&reinterpret_cast<Stage *>(attn_smem)[w].hist[0][0])[i];
+        (&sh.hist[0][0])[i] = n;
+    }
     cg::cluster_group cluster = cg::this_cluster();
     if (C > 1) cluster.sync();
     else __syncthreads();
@@ -475,7 +486,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                         below[e] += o0 + o < rank ? x[o][e] : 0;
                     }
             }
-            int *const to = reinterpret_cast<int *>(stage.codes);
+            int *const to = reinterpret_cast<int *>(&stage.terms);          // 64 EL words
 #pragma unroll
             for (int e = 0; e < EL; ++e) {
                 to[lane + 32 * e] = all[e];
@@ -582,7 +593,15 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         }
         // ties of each row in this warp's part, where a row keeps only some
         int before = 0, all = 0, here = 0;
-        if (sh.ranked) {
+        if (!kLong && sh.ranked && lane < rows && my_level >= 0) {
+            for (int w = 0; w < W; ++w) {
+                const int x = reinterpret_cast<Stage *>(attn_smem)[w].hist[lane][my_level];
+                before += w < warp ? x : 0;
+                here = w == warp ? x : here;
+            }
+        }
+        if (!kLong) __syncthreads();          // the counts make room for the copies
+        if (kLong && sh.ranked) {             // counts of one segment
             for (int q = 0; q < RW; ++q) {
                 uint32_t same = 0;
 #pragma unroll
