@@ -437,7 +437,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         }
     };
     // a warp's part of n keys: whole groups of 32, in key order
-    auto warp_begin = [&](int n, int w) { return min(n, w * (((n + kThreads - 1) / kThreads) * 32)); };
+    auto warp_begin = [&](int n, int w) { return min(n, (((n + 31) >> 5) * w / W) << 5); };
 
     for (int seg = 0; seg < segs; ++seg) {
         const int s0 = u0 + seg * cap, n = min(cap, u1 - s0);
@@ -609,7 +609,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                     const int l = __shfl_sync(kFullMask, my_level, 4 * q + i);
                     same |= (l < 0 ? 0xffu : (uint32_t)l) << (8 * i);
                 }
-                uint32_t mine = 0;                // a byte per row: at most cap / 128 keys a lane
+                uint32_t mine = 0;                // a byte per row: at most cap / 128 + 1 keys a lane
                 for (int k = wb + lane; k < we; k += 32)
                     mine += __vcmpeq4(distw[q * cap + k], same) & 0x01010101u;
 #pragma unroll
