@@ -195,11 +195,11 @@ had_status_t check_rows(int B, int heads, int T)
 }
 
 // Rows (b, head, token) of an append or a read, and the grid that has `lanes`
-// threads for kCacheRows of them.
+// threads for `at_once` of them.
 CacheTokens tokens_of(const int32_t *table, int max_pages, const int32_t *start,
-                      const int32_t *counts, int B, int heads, int T, int lanes, unsigned *grid)
+                      const int32_t *counts, int B, int heads, int T, int lanes, int at_once, unsigned *grid)
 {
-    const unsigned rows = (unsigned)B * heads * T, per = 256 / lanes * had::kCacheRows;
+    const unsigned rows = (unsigned)B * heads * T, per = 256 / lanes * at_once;
     *grid = (rows + per - 1) / per;
     return CacheTokens{table, start, counts, max_pages, T, rows, had::divisor(T),
                        had::divisor(heads)};
@@ -227,7 +227,7 @@ had_status_t had_cache_append(const void *K, const void *V, had_dtype_t dt, cons
         return HAD_ERR_INVALID_ARG;
     unsigned grid;
     const CacheTokens k = tokens_of(table, max_pages, start, counts, B, c.heads, T,
-                                    had::kCacheLanes, &grid);
+                                    had::kCacheLanes, had::kCacheRows, &grid);
     if (dt == HAD_BF16)
         launch_append<__nv_bfloat16>(K, V, sigma_k, c, cache->d, k, grid, dev_status, stream);
     else
@@ -251,7 +251,7 @@ had_status_t had_cache_read(const had_cache_t *cache, const int32_t *table, int 
     if (!bits && !values) return HAD_ERR_INVALID_ARG;
     unsigned grid;
     const CacheTokens k = tokens_of(table, max_pages, start, counts, B, c.heads, T,
-                                    had::kReadLanes, &grid);
+                                    had::kReadLanes, had::kReadRows, &grid);
     if (cache->d == 64)
         had::cache_read_kernel<64><<<grid, 256, 0, stream>>>(c, k, bits, values, dev_status);
     else

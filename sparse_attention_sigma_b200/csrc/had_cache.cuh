@@ -113,8 +113,8 @@ __device__ __forceinline__ unsigned divide(unsigned n, const Divisor &d)
     return (__umulhi(n, d.mul) + n) >> d.shift;
 }
 
-constexpr int kCacheLanes = 8;         // threads of one (token, head) row
-constexpr int kCacheRows = 2;          // rows of a thread whose loads are in flight together
+constexpr int kCacheLanes = 4;         // threads of one (token, head) row
+constexpr int kCacheRows = 1;          // rows of a thread whose loads are in flight together
 
 // Where the tokens of an append or a read lie: row i of rows = (b, head, t).
 struct CacheTokens {
@@ -220,18 +220,17 @@ struct CacheSlice {
 // it sees NaN.
 //
 // HBM-bound once the arithmetic is lean: 2 d elements read, d/8 + d/2 + 4
-// bytes written per row.  8 lanes take a row, two rows are in flight: what a row
-// costs once (place, scale, quotients: about 130 instructions) is shared by
-// E = d / 8 elements a lane.  The extremes are joined by three shuffles and a
-// word of signs by the 32 / E lanes that hold its elements.  Element-wise
-// arithmetic takes two values an instruction.  A quotient is x y with y = 1 / s
-// rounded, corrected once by its exact remainder, which makes it the rounded
-// quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990, theorem 7).  No lane leaves early: the shuffles
-// then name the whole warp, and half-warp masks cost more than all of the
-// arithmetic (197 k rows of d 128, bf16: 80 us so, 57 us with whole warps and 16
-// lanes a row, 46 us with 8 and divisions beside a half, 36 us now; 20 us of
-// HBM time).
+// bytes written per row.  4 lanes take a row: what a row costs once (place,
+// scale, checks: about 200 instructions) is shared by E = d / 4 elements a lane.
+// The extremes are joined by two shuffles and a word of signs by the 32 / E lanes
+// that hold its elements.  Element-wise arithmetic takes two values an
+// instruction.  A quotient is x y with y = 1 / s rounded, corrected once by its
+// exact remainder, which makes it the rounded quotient (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990, theorem 7).  No lane leaves early: the shuffles then name the whole warp,
+// and half-warp masks cost more than all of the arithmetic.  229 k rows of d 128,
+// bf16: 80 us with those, 57 us with whole warps and 16 lanes a row, 46 us with 8
+// and a division beside each half, 36 us without, 29 us now; 21 us of HBM time.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
 cache_append_kernel(const T *__restrict__ K, const T *__restrict__ V,
@@ -314,10 +313,11 @@ cache_append_kernel(const T *__restrict__ K, const T *__restrict__ V,
         }
         if (here) {
             uint32_t *const to = reinterpret_cast<uint32_t *>(c.vcodes) + (size_t)at[i] * (D / 8) + l * (E / 8);
-            if constexpr (E == 16)
-                *reinterpret_cast<uint2 *>(to) = coded ? make_uint2(codes[0], codes[1]) : make_uint2(0u, 0u);
+            if constexpr (E == 32)
+                *reinterpret_cast<uint4 *>(to) = coded ? make_uint4(codes[0], codes[1], codes[2], codes[3])
+                                                       : make_uint4(0u, 0u, 0u, 0u);
             else
-                *to = coded ? codes[0] : 0u;
+                *reinterpret_cast<uint2 *>(to) = coded ? make_uint2(codes[0], codes[1]) : make_uint2(0u, 0u);
             if (l == 0)
                 c.vscale[at[i]] = fine ? (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xffff0000u)
                                        : 0x7fc07fc0u;
@@ -327,10 +327,10 @@ cache_append_kernel(const T *__restrict__ K, const T *__restrict__ V,
 
 // Tokens of the cache as packed signs and fp32 values c s + z (one FMA:
 // rounded once); zeros for tokens beyond a sequence's count.  HBM-bound by
-// the 4 d bytes written per row; 16 lanes a row, each D / 64 times 16 bytes of
-// consecutive lanes, two rows in flight (30 us for 262 k rows of d 128, of
-// which 197 k are there; 24 us of HBM time).
-constexpr int kReadLanes = 16;
+// the 4 d bytes written per row; 8 lanes a row, each D / 32 times 16 bytes of
+// consecutive lanes, two rows in flight (262 k rows of d 128, of which 229 k are
+// there: 27 us, with 16 lanes a row 30 us; 24 us of HBM time).
+constexpr int kReadLanes = 8, kReadRows = 2;
 
 template <int D>
 __global__ void __launch_bounds__(256)
@@ -341,13 +341,13 @@ cache_read_kernel(CacheView c, CacheTokens k, uint32_t *__restrict__ bits,
     const int l = threadIdx.x & (kReadLanes - 1);
     const unsigned step = gridDim.x * (256u / kReadLanes);
     const unsigned row0 = (blockIdx.x * 256u + threadIdx.x) / kReadLanes;
-    uint32_t at[kCacheRows];
-    uint32_t codes[kCacheRows][E / 4], sz[kCacheRows], word[kCacheRows];
+    uint32_t at[kReadRows];
+    uint32_t codes[kReadRows][E / 4], sz[kReadRows], word[kReadRows];
 #pragma unroll
-    for (int i = 0; i < kCacheRows; ++i)
+    for (int i = 0; i < kReadRows; ++i)
         at[i] = cache_place(c, k, cache_token(k, row0 + i * step, status), status);
 #pragma unroll
-    for (int i = 0; i < kCacheRows; ++i) {
+    for (int i = 0; i < kReadRows; ++i) {
         const bool here = at[i] != kNoRow;
         word[i] = here && bits && l < D / 32 ? __ldg(c.kbits + (size_t)at[i] * (D / 32) + l) : 0u;
         sz[i] = here && values ? __ldg(c.vscale + at[i]) : 0u;
@@ -357,7 +357,7 @@ cache_read_kernel(CacheView c, CacheTokens k, uint32_t *__restrict__ bits,
                                                  (size_t)at[i] * (D / 4) + e * kReadLanes + l) : 0u;
     }
 #pragma unroll
-    for (int i = 0; i < kCacheRows; ++i) {
+    for (int i = 0; i < kReadRows; ++i) {
         const unsigned row = row0 + i * step;
         if (row >= k.rows) break;
         if (bits && l < D / 32) bits[(long long)row * (D / 32) + l] = word[i];
