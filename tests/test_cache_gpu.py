@@ -529,9 +529,11 @@ def test_books_through_a_run(cache, S, width, P, page, seed):
         assert np.array_equal(counted, refs.cpu().numpy())
 
 
-def test_books_of_a_large_pool(cache):
-    """More pages and sequences than one pass of a CTA over them covers."""
-    S, width, P, page = 3000, 20, 70001, 16
+@pytest.mark.parametrize("S,width,P", [(3000, 20, 70001), (8192, 7, 60000)])
+def test_books_of_a_large_pool(cache, S, width, P):
+    """More pages and sequences than one pass of a CTA over them covers, up to the most there may
+    be."""
+    page = 16
     g = np.random.default_rng(11)
     table, lens, refs = cache.empty_books(S, width, P)
     b = ocache.Books(table, lens, refs, page)
