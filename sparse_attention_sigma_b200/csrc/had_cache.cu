@@ -27,6 +27,13 @@ had_status_t launched()
     return cudaGetLastError() == cudaSuccess ? HAD_OK : HAD_ERR_CUDA;
 }
 
+// A call that failed: its error is not left for the caller's next check.
+had_status_t failed()
+{
+    cudaGetLastError();
+    return HAD_ERR_CUDA;
+}
+
 bool good_page(int page)
 {
     return page == 16 || page == 32 || page == 64 || page == 128 || page == 256;
@@ -85,7 +92,7 @@ had_status_t launch_clusters(void (*kernel)(Params...), unsigned grid, unsigned 
     if (smem > 24 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
             cudaSuccess)
-        return HAD_ERR_CUDA;
+        return failed();
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim = {ctas, 1, 1};
@@ -97,7 +104,7 @@ had_status_t launch_clusters(void (*kernel)(Params...), unsigned grid, unsigned 
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
-    return e == cudaSuccess ? launched() : HAD_ERR_CUDA;
+    return e == cudaSuccess ? launched() : failed();
 }
 
 // A launch of one cluster of the page operators.
@@ -141,14 +148,17 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStrea
     const long long tiles = (long long)B * a.c.heads * plan.tiles;
     // 20 KB of distances at once, so that four CTAs share an SM
     constexpr long long most = 20 * 1024 / (4 * RW) / 128 * 128;
-    // CTAs until four per SM are busy, each with 512 keys or more, and until a
-    // CTA holds its slice whole (a longer one is gone through twice).  Measured
-    // with 1, 2, 4 and 8: 64 tiles of 4 k keys 39, 24, 15.7, 15.0 us; 128 of
-    // 16 k 216, 131, 74, 80 us; 256 of 1028 23.8, 22.9, 32, 60 us; one of 128
-    // keys 6.4, 7.7, 7.4, 8.0 us.
-    while (plan.ctas < had::kMaxCtas &&
-           (keys > most * plan.ctas ||
-            (tiles * plan.ctas * 2 <= 4 * 148 && keys > 512LL * plan.ctas)))
+    // CTAs until four per SM are busy, each with 512 keys or more; the device uses
+    // fewer for a tile that has fewer keys.  Measured with 1, 2, 4 and 8: 64 tiles
+    // of 4 k keys 38, 23, 15.0, 15.2 us; 128 of 16 k 211, 129, 67, 73 us; 256 of
+    // 1028 22.5, 21.5, 31, 58 us; one of 128 keys 6.4, 7.7, 7.4, 8.0 us.  Not more
+    // CTAs where the table's rows hold more keys than fit the CTAs' memory: those
+    // are gone through twice, if they are there (1024 tiles of 16 k keys 608 us
+    // instead of 428), but often a table is wider than its sequences, and a cluster
+    // keeps its places until its last CTA is done (512 tiles of 4 k keys in a
+    // table for 128 k: 71 us, with 4 CTAs 94, with 8 149 us).
+    while (plan.ctas < had::kMaxCtas && tiles * plan.ctas * 2 <= 4 * 148 &&
+           keys > 512LL * plan.ctas)
         plan.ctas *= 2;
     const long long per = (keys + plan.ctas - 1) / plan.ctas;
     return per <= most ? launch_attention_plan<D, RW, false>(a, tiles, plan, per, st)

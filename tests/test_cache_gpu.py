@@ -334,6 +334,26 @@ def test_long_contexts(cache, d, n, G, T, N, window):
     assert (np.abs(out.cpu().numpy() - want) <= bound).all()
 
 
+@pytest.mark.parametrize("lens,H,G,T,d,N,window", [
+    ([2100, 0, 700, 1], 2, 2, 1, 64, 90, 0), ([5000, 300], 1, 3, 2, 128, 400, 0),
+    ([6000, 900, 37], 2, 8, 1, 128, 100, 0), ([3000, 12000], 1, 1, 1, 64, 5000, 0),
+    ([3000, 250], 1, 4, 9, 64, 50, 2000)])
+def test_tables_much_wider_than_their_sequences(cache, lens, H, G, T, d, N, window):
+    """The launch is made for as many keys as a table row may hold, the work for those that are
+    there."""
+    f = Filled(cache, lens, H, d, 16, BF16, seed=sum(lens))
+    q, sigma_q = queries(len(lens), H * G, T, d, BF16)
+    want, bound = f.rows(q, sigma_q, lens, [T] * len(lens), N, 0.1, window, 4)
+    for width in (1000, 70000):
+        table = torch.full((len(lens), width), -1, dtype=I, device="cuda")
+        table[:, :f.table.shape[1]] = f.table
+        st = status()
+        out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, table, ints(lens), N,
+                                        0.1, window=window, sinks=4, dev_status=st)
+        assert flags(st) == 0
+        assert (np.abs(out.cpu().numpy() - want) <= bound).all()
+
+
 @pytest.mark.parametrize("B,H,G,T,d,n,window", [
     (16, 16, 1, 80, 64, 90, 0), (35, 61, 3, 1, 128, 50, 20), (16, 17, 2, 32, 128, 70, 33),
     (40, 53, 1, 3, 64, 40, 0)])
