@@ -456,6 +456,10 @@ HAD_API had_status_t had_cache_read(const had_cache_t *cache, const int32_t *tab
  *   N       >= 1: kept keys per row; a row with fewer visible keys keeps all
  *   window  0, or W >= 1: position i sees j <= i with j > i - W or j < sinks
  *   sinks   >= 0: first tokens that stay visible under a window
+ *   max_len 0, or the most tokens that the caller expects in lens: a hint for
+ *           the launch, which knows the table's width only.  It changes the
+ *           speed of many long sequences, and of a result at most the rounding;
+ *           lens may pass it.
  *   out     [B, Hq, T, d] float
  * The rule of had_attention_causal_fwd at position i = lens[b] - counts[b] +
  * t, over the cached signs and values.  Rows at or behind counts[b], at a
@@ -466,8 +470,8 @@ HAD_API had_status_t had_cache_attention(const void *Q, had_dtype_t dt, const fl
                                          const had_cache_t *cache, const int32_t *table,
                                          int max_pages, const int32_t *lens,
                                          const int32_t *counts, int B, int Hq, int T, int N,
-                                         float tau, int window, int sinks, float *out,
-                                         int32_t *dev_status, cudaStream_t stream);
+                                         float tau, int window, int sinks, int max_len,
+                                         float *out, int32_t *dev_status, cudaStream_t stream);
 
 /*
  * Forking: sequence dst[i] lets its pages go and continues as a copy of

@@ -135,13 +135,14 @@ def had_cache_read(cache, table, start, T, counts=None, bits=None, values=None, 
 
 
 def had_cache_attention(q, sigma_q, cache, table, lens, N, tau, window=0, sinks=0, counts=None,
-                        out=None, dev_status=None, stream=None):
+                        out=None, dev_status=None, stream=None, max_len=0):
     """Attention of the newest tokens q [B, Hq, T, d] (of which counts[b], default all) to the
     lens[b] cached ones: the N best visible keys, within `window` positions and the first
-    `sinks` tokens if window > 0; returns out [B, Hq, T, d] float32."""
+    `sinks` tokens if window > 0; returns out [B, Hq, T, d] float32.  max_len: what lens is
+    expected not to pass, a hint that speeds up many long sequences."""
     return _call(_native.attention, "had_cache_attention",
                  (_of(cache), q, sigma_q, table, lens, N, tau, window, sinks, counts, out,
-                  dev_status), stream, q)[0]
+                  dev_status, max_len), stream, q)[0]
 
 
 def had_cache_fork(table, lens, refs, page, src, dst, dev_status=None, stream=None):

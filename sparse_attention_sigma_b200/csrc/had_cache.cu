@@ -131,7 +131,7 @@ had_status_t launch_attention_plan(const had::CacheAttnArgs &a, long long tiles,
 }
 
 template <int D, int RW>
-had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStream_t st)
+had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, int max_len, cudaStream_t st)
 {
     const long long rows = (long long)(a.Hq / a.c.heads) * a.T;      // per key-value head
     had::CacheAttnPlan plan{};
@@ -151,14 +151,16 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStrea
     // CTAs until four per SM are busy, each with 512 keys or more; the device uses
     // fewer for a tile that has fewer keys.  Measured with 1, 2, 4 and 8: 64 tiles
     // of 4 k keys 38, 23, 15.0, 15.2 us; 128 of 16 k 211, 129, 67, 73 us; 256 of
-    // 1028 22.5, 21.5, 31, 58 us; one of 128 keys 6.4, 7.7, 7.4, 8.0 us.  Not more
-    // CTAs where the table's rows hold more keys than fit the CTAs' memory: those
-    // are gone through twice, if they are there (1024 tiles of 16 k keys 608 us
-    // instead of 428), but often a table is wider than its sequences, and a cluster
-    // keeps its places until its last CTA is done (512 tiles of 4 k keys in a
-    // table for 128 k: 71 us, with 4 CTAs 94, with 8 149 us).
-    while (plan.ctas < had::kMaxCtas && tiles * plan.ctas * 2 <= 4 * 148 &&
-           keys > 512LL * plan.ctas)
+    // 1028 22.5, 21.5, 31, 58 us; one of 128 keys 6.4, 7.7, 7.4, 8.0 us.  More
+    // CTAs, until their memory holds a tile's keys whole, only for as many keys as
+    // the caller says there are: keys that do not fit are gone through twice (1024
+    // tiles of 16 k keys 608 us instead of 428), but a table is often wider than
+    // its sequences, and a cluster keeps its places until its last CTA is done (512
+    // tiles of 4 k keys in a table for 128 k: 71 us, with 4 CTAs 94, with 8 149 us).
+    const long long expected = max_len < keys ? max_len : keys;
+    while (plan.ctas < had::kMaxCtas &&
+           (expected > most * plan.ctas ||
+            (tiles * plan.ctas * 2 <= 4 * 148 && keys > 512LL * plan.ctas)))
         plan.ctas *= 2;
     const long long per = (keys + plan.ctas - 1) / plan.ctas;
     return per <= most ? launch_attention_plan<D, RW, false>(a, tiles, plan, per, st)
@@ -172,12 +174,12 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, cudaStrea
 // 68; 16 decodes of 4 k tokens, 8 query heads to a key head, 16.8, 20 us;
 // d 128: 91, 89; 74, 55; 20, 27 us.
 template <int D>
-had_status_t launch_attention(const had::CacheAttnArgs &a, int B, cudaStream_t st)
+had_status_t launch_attention(const had::CacheAttnArgs &a, int B, int max_len, cudaStream_t st)
 {
     const long long rows = (long long)(a.Hq / a.c.heads) * a.T;
     if (rows > 4 && (rows + 7) / 8 * B * a.c.heads * 4 >= 3 * 148)
-        return launch_attention_tile<D, 2>(a, B, st);
-    return launch_attention_tile<D, 1>(a, B, st);
+        return launch_attention_tile<D, 2>(a, B, max_len, st);
+    return launch_attention_tile<D, 1>(a, B, max_len, st);
 }
 
 unsigned grid_for(long long items, int per_block)
@@ -272,7 +274,7 @@ had_status_t had_cache_read(const had_cache_t *cache, const int32_t *table, int 
 had_status_t had_cache_attention(const void *Q, had_dtype_t dt, const float *sigma_q,
                                  const had_cache_t *cache, const int32_t *table, int max_pages,
                                  const int32_t *lens, const int32_t *counts, int B, int Hq, int T,
-                                 int N, float tau, int window, int sinks, float *out,
+                                 int N, float tau, int window, int sinks, int max_len, float *out,
                                  int32_t *dev_status, cudaStream_t stream)
 {
     CacheView c;
@@ -281,7 +283,8 @@ had_status_t had_cache_attention(const void *Q, had_dtype_t dt, const float *sig
     if (s == HAD_OK) s = check_rows(B, Hq, T);
     if (s == HAD_OK) s = check_table(table, B, max_pages, cache->page);
     if (s != HAD_OK) return s;
-    if (Hq % c.heads != 0 || N < 1 || window < 0 || sinks < 0 || !finite_nonneg(tau))
+    if (Hq % c.heads != 0 || N < 1 || window < 0 || sinks < 0 || max_len < 0 ||
+        !finite_nonneg(tau))
         return HAD_ERR_INVALID_ARG;
     if (dt != HAD_BF16 && dt != HAD_F32) return HAD_ERR_INVALID_ARG;
     if (!good(Q, 16) || !good(out, 16) || !good(sigma_q, 4) || !good(lens, 4) ||
@@ -289,7 +292,8 @@ had_status_t had_cache_attention(const void *Q, had_dtype_t dt, const float *sig
         return HAD_ERR_INVALID_ARG;
     const had::CacheAttnArgs a{Q, dt == HAD_BF16, sigma_q, c, table, lens, counts, max_pages, Hq, T, N, window,
                                sinks, tau, out, dev_status};
-    return cache->d == 64 ? launch_attention<64>(a, B, stream) : launch_attention<128>(a, B, stream);
+    return cache->d == 64 ? launch_attention<64>(a, B, max_len, stream)
+                          : launch_attention<128>(a, B, max_len, stream);
 }
 
 had_status_t had_cache_fork(int32_t *table, int32_t *lens, int32_t *refs, int S, int max_pages,

@@ -250,7 +250,7 @@ PyObject *call_read(PyObject *const *a)
     return with_outputs(s, bits, values);
 }
 
-// pool, q, sigma_q, table, lens, N, tau, window, sinks, counts, out, dev_status
+// pool, q, sigma_q, table, lens, N, tau, window, sinks, counts, out, dev_status, max_len
 PyObject *call_attention(PyObject *const *a)
 {
     const Pool &p = pool_of(a[0]);
@@ -270,12 +270,13 @@ PyObject *call_attention(PyObject *const *a)
         type_error("tau must be a number");
     }
     const int window = number(a[7], "window"), sinks = number(a[8], "sinks");
+    const int max_len = number(a[12], "max_len");
     const int32_t *counts = maybe_ints(a[9], "counts", B, p.device);
     int32_t *status = maybe_ints(a[11], "dev_status", 1, p.device);
     On on(p.device);
     const Tensor out = output(a[10], "out", ScalarType::Float, q.sizes(), p.device);
     const had_status_t s = had_cache_attention(q.data_ptr(), dt, sigma, &p.c, table, width, lens, counts,
-                                               B, Hq, T, N, (float)tau, window, sinks,
+                                               B, Hq, T, N, (float)tau, window, sinks, max_len,
                                                static_cast<float *>(out.data_ptr()), status, on.stream);
     return with_outputs(s, out);
 }
@@ -406,7 +407,7 @@ PyMethodDef method(const char *name)
 
 PyMethodDef methods[] = {
     method<make_pool, 3>("pool"),       method<call_append, 8>("append"),
-    method<call_read, 8>("read"),            method<call_attention, 12>("attention"),
+    method<call_read, 8>("read"),            method<call_attention, 13>("attention"),
     method<call_fork, 7>("fork"),            method<call_reserve, 8>("reserve"),
     method<call_free, 5>("free"),       method<call_evict, 7>("evict"),
     method<call_compact, 6>("compact"),      method<call_copy_pages, 4>("copy_pages"),

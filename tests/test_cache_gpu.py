@@ -348,10 +348,12 @@ def test_tables_much_wider_than_their_sequences(cache, lens, H, G, T, d, N, wind
         table = torch.full((len(lens), width), -1, dtype=I, device="cuda")
         table[:, :f.table.shape[1]] = f.table
         st = status()
-        out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, table, ints(lens), N,
-                                        0.1, window=window, sinks=4, dev_status=st)
-        assert flags(st) == 0
-        assert (np.abs(out.cpu().numpy() - want) <= bound).all()
+        for max_len in (0, max(lens), 1, 2 ** 31 - 1):           # a hint, right or wrong
+            out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, table, ints(lens),
+                                            N, 0.1, window=window, sinks=4, dev_status=st,
+                                            max_len=max_len)
+            assert flags(st) == 0
+            assert (np.abs(out.cpu().numpy() - want) <= bound).all()
 
 
 @pytest.mark.parametrize("B,H,G,T,d,n,window", [
@@ -801,6 +803,7 @@ def test_refusals_of_the_binding(cache):
             (dict(counts=ints([1, 1])), ValueError), (dict(N=0), cache.HadError),
             (dict(tau=-1.0), cache.HadError), (dict(window=-1), cache.HadError),
             (dict(window=2 ** 31), ValueError), (dict(sinks=-1), cache.HadError),
+            (dict(max_len=-1), cache.HadError),
             (dict(out=torch.zeros(1, 4, 1, 64)), ValueError), (dict(cache=f.cache.kbits), TypeError),
             (dict(q=q[:, :3].contiguous(), sigma_q=s[:3]), cache.HadError),
             (dict(dev_status=torch.zeros(2, dtype=I, device="cuda")), ValueError)):

@@ -32,7 +32,7 @@ def _library():
             "had_cache_append": [vp, vp, i32, vp, pl, vp, i32, vp, vp, i32, i32, vp, vp],
             "had_cache_read": [pl, vp, i32, vp, vp, i32, i32, vp, vp, vp, vp],
             "had_cache_attention": [vp, i32, vp, pl, vp, i32, vp, vp, i32, i32, i32, i32, f32, i32,
-                                    i32, vp, vp, vp],
+                                    i32, i32, vp, vp, vp],
             "had_cache_fork": [vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp, vp],
             "had_cache_reserve": [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp],
             "had_cache_free": [vp, vp, vp, i32, i32, i32, vp, i32, vp, vp],
@@ -61,7 +61,8 @@ APPEND = dict(k=FAKE, v=FAKE, dt=0, sigma=FAKE, pool=pool(), table=FAKE, width=4
 READ = dict(pool=pool(), table=FAKE, width=4, start=FAKE, counts=None, B=1, T=1, bits=FAKE,
             values=FAKE, status=None, stream=None)
 ATTEND = dict(q=FAKE, dt=0, sigma=FAKE, pool=pool(), table=FAKE, width=4, lens=FAKE, counts=None,
-              B=1, Hq=2, T=1, N=4, tau=0.1, window=0, sinks=0, out=FAKE, status=None, stream=None)
+              B=1, Hq=2, T=1, N=4, tau=0.1, window=0, sinks=0, max_len=0, out=FAKE, status=None,
+              stream=None)
 FORK = dict(table=FAKE, lens=FAKE, refs=FAKE, S=4, width=4, pages=8, page=16, src=FAKE, dst=FAKE,
             n=1, status=None, stream=None)
 RESERVE = dict(table=FAKE, lens=FAKE, refs=FAKE, S=4, width=4, pages=8, page=16, grow=FAKE,
@@ -100,6 +101,7 @@ REFUSALS = {
         (dict(Hq=3), INVALID), (dict(Hq=0), INVALID), (dict(N=0), INVALID),
         (dict(tau=-0.5), INVALID), (dict(tau=float("nan")), INVALID),
         (dict(tau=float("inf")), INVALID), (dict(window=-1), INVALID), (dict(sinks=-1), INVALID),
+        (dict(max_len=-1), INVALID),
         (dict(T=0), INVALID), (dict(B=2 ** 15, T=2 ** 16), UNSUPPORTED)]),
     "had_cache_fork": (FORK, BOOKS + PAGES + [
         (dict(lens=None), INVALID), (dict(src=None), INVALID), (dict(dst=4098), INVALID),
