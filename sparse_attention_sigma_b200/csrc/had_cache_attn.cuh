@@ -309,12 +309,13 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         max_lo = to.lo;
         if (t_first == t_lo && t_last == t_hi) min_pos = from.pos;
     }
-    // The CTAs that this tile uses, one per 512 keys; the others leave at once (a
-    // cluster's barriers wait for those that are there).  The host knows no lengths
-    // and launches for as many keys as a row of the table may hold (one sequence of
-    // 200 tokens in a table for 128 k: 8.4 us, with all eight CTAs 9.7 us).
+    // The CTAs that this tile uses, one per 512 keys or per `cap`, which may be
+    // less; the others leave at once (a cluster's barriers wait for those that are
+    // there).  The host knows no lengths and launches for as many keys as a row of
+    // the table may hold (one sequence of 200 tokens in a table for 128 k: 8.4 us,
+    // with all eight CTAs 9.7 us).
     int C = 1;
-    while (C < plan.ctas && total > 512 * C) C *= 2;
+    while (C < plan.ctas && total > min(512, cap) * C) C *= 2;
     if (rank >= C) return;
 
 #pragma unroll

@@ -334,6 +334,23 @@ def test_long_contexts(cache, d, n, G, T, N, window):
     assert (np.abs(out.cpu().numpy() - want) <= bound).all()
 
 
+@pytest.mark.parametrize("longest", [513, 600, 1040, 1100, 2064, 2784])
+@pytest.mark.parametrize("G,d", [(1, 64), (7, 128)])
+def test_lengths_about_what_a_cta_holds(cache, longest, G, d):
+    """A launch for the longest sequence splits it over CTAs that hold little more than their part;
+    shorter sequences beside it use fewer of them."""
+    lens = [longest, 512, 500, 400, 385, 384, 383, 300, 257, 256, longest // 2, longest // 2 + 1]
+    f = Filled(cache, lens, 1, d, 16, BF16, seed=longest)
+    q, sigma_q = queries(len(lens), G, 1, d, BF16)
+    st = status()
+    table = f.table[:, :-(-longest // 16)].contiguous()
+    out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, table, ints(lens), 200, 0.1,
+                                    dev_status=st)
+    assert flags(st) == 0
+    want, bound = f.rows(q, sigma_q, lens, [1] * len(lens), 200, 0.1, 0, 0)
+    assert (np.abs(out.cpu().numpy() - want) <= bound).all()
+
+
 @pytest.mark.parametrize("lens,H,G,T,d,N,window", [
     ([2100, 0, 700, 1], 2, 2, 1, 64, 90, 0), ([5000, 300], 1, 3, 2, 128, 400, 0),
     ([6000, 900, 37], 2, 8, 1, 128, 100, 0), ([3000, 12000], 1, 1, 1, 64, 5000, 0),
