@@ -396,7 +396,7 @@ HAD_API size_t had_noalloc_scratch_bytes(void);
  *             low nibble of byte i, element 2i + 1 in the high one
  *     vscale  [pages, heads, page, 2] bf16: s, then z
  *     page    16, 32, 64, 128 or 256;  d 64 or 128
- *     pages * heads * page < 2^32
+ *     pages * heads * page < 2^32;  pages < 2^31 - 2^16
  *   table   [S, max_pages] int32 (device): pages of sequence s in order, -1
  *           for none.  max_pages * page < 2^31 - 2^16.
  *   lens    [S] int32: tokens of a sequence;  refs [pages] int32: how many

@@ -77,6 +77,7 @@ had_status_t check_books(int32_t *table, const int32_t *lens, int32_t *refs, int
 {
     if (pages < 1 || !good(lens, 4) || !good(refs, 4)) return HAD_ERR_INVALID_ARG;
     if (page != 1 && !good_page(page)) return HAD_ERR_UNSUPPORTED;
+    if (pages > INT_MAX - 65536) return HAD_ERR_UNSUPPORTED;     // a CTA's step past the last is an int
     const had_status_t s = check_table(table, S, max_pages, page);
     *books = Books{table, const_cast<int32_t *>(lens), refs, S, max_pages, pages, log2_of(page)};
     return s;

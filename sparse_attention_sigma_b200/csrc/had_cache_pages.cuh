@@ -462,7 +462,7 @@ cache_copy_kernel(CacheView c, CopyWords words, const int32_t *__restrict__ src,
                   const int32_t *__restrict__ dst, int n, int32_t *status)
 {
     const int lane = threadIdx.x & 31;
-    for (int i0 = blockIdx.y; i0 < n; i0 += 32 * gridDim.y) {
+    for (long long i0 = blockIdx.y; i0 < n; i0 += 32LL * gridDim.y) {
         const long long i = i0 + (long long)lane * gridDim.y;
         const int s = i < n ? __ldg(src + i) : -1, d = i < n ? __ldg(dst + i) : -1;
         const bool pair = s >= 0 && d >= 0, good = pair && s < c.pages && d < c.pages;

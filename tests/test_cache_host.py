@@ -83,7 +83,8 @@ POOLS = [(dict(pool=None), INVALID), (dict(pool=pool(d=96)), UNSUPPORTED),
          (dict(pool=pool(pages=2 ** 31 - 1, heads=2 ** 16)), UNSUPPORTED)]
 TABLES = [(dict(table=None), INVALID), (dict(table=4098), INVALID), (dict(width=0), INVALID),
           (dict(width=2 ** 27), UNSUPPORTED)]
-BOOKS = TABLES[:3] + [(dict(refs=None), INVALID), (dict(S=0), INVALID), (dict(pages=0), INVALID)]
+BOOKS = TABLES[:3] + [(dict(refs=None), INVALID), (dict(S=0), INVALID), (dict(pages=0), INVALID),
+                      (dict(pages=2 ** 31 - 1), UNSUPPORTED)]
 PAGES = [(dict(page=0), UNSUPPORTED), (dict(page=1), UNSUPPORTED), (dict(page=48), UNSUPPORTED)]
 
 REFUSALS = {
