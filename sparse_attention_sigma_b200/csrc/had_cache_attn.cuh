@@ -585,6 +585,14 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         }
         return f;
     };
+    // what was summed under the rows' scales of before
+    auto shrink_sums = [&]() {
+        const float f = of_row_g(shrink);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] *= f;
+    };
     // lane r < rows follows row r's level and the ties it may still keep
     const int my_level = lane < rows ? sh.level[lane] : -1;
     int my_quota = lane < rows ? sh.quota[lane] : 0;
@@ -792,7 +800,8 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
         }
         asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
         __syncwarp();
-        if (queued > 0) weigh(0);
+        // (in the first segment nothing was summed before: what it returns does not matter)
+        if (queued > 0 && weigh(0) && kLong) shrink_sums();
         // Step c issues the copies of chunk c + 3, weighs chunk c + 1 and
         // multiplies chunk c: the last two are independent, and one warp barrier
         // stands between a step's writes and the next step's reads.
@@ -828,13 +837,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                     mma_f16(acc[8 * w + 2 * byte], af, codes_low(x0, raised), codes_low(x1, raised));
                     mma_f16(acc[8 * w + 2 * byte + 1], af, codes_high(x0, raised), codes_high(x1, raised));
                 }
-            if (__builtin_expect(smaller, 0)) {            // the next chunk's scale
-                const float f = of_row_g(shrink);
-#pragma unroll
-                for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][e] *= f;
-            }
+            if (__builtin_expect(smaller, 0)) shrink_sums();       // the next chunk's scale
         }
         __syncwarp();
     }

@@ -844,3 +844,93 @@ def test_refusals_of_the_binding(cache):
         cache.Cache(f.cache.kbits, f.cache.vcodes[:, :1].contiguous(), f.cache.vscale)
     with pytest.raises(cache.HadError):
         cache.had_cache_read(f.cache, f.table, ints([0]), 0)
+
+
+# ------------------------------------------- slices that pass a CTA's memory
+
+def _grown(size):
+    """Values of unit noise times size(j, n) at token j of n."""
+    def values(B, H, T, d):
+        g = torch.Generator().manual_seed(T + d)
+        return torch.randn(B, H, T, d, generator=g) * size(torch.arange(T, dtype=torch.float64), T)[:, None]
+    return values
+
+
+SIZES = {
+    "grow": lambda j, n: 10.0 ** (6 * j / n),
+    "fall": lambda j, n: 10.0 ** (-6 * j / n),
+    "last_grow": lambda j, n: torch.where(j < 0.85 * n, 0.2, 1.2),
+    "step": lambda j, n: 8.0 ** torch.floor(5 * j / n),
+    "swing": lambda j, n: 10.0 ** (8 * torch.sin(j / n * 40)),
+}
+
+
+# 300 tiles or more with one CTA each, which holds 5120 keys in tiles of four
+# rows and 2560 in tiles of eight: every instance of the path with segments
+@pytest.mark.parametrize("B,G,T,n", [(300, 1, 1, 11000), (1, 3, 800, 6000)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", sorted(SIZES))
+def test_values_that_change_size_between_segments(cache, d, B, G, T, n, size):
+    """What was summed in earlier segments follows the row's scale in the later ones.  (Sequences
+    of one prompt share its pages; the oracle goes through every 37th row.)"""
+    f = Filled(cache, [n], 1, d, 64, F32, seed=n + d, values=_grown(SIZES[size]))
+    table = f.table.repeat(B, 1)
+    lens = [n - 17 * b for b in range(B)]
+    q, sigma_q = queries(B, G, T, d, F32)
+    for N, tau in ((n, 0.0), (n, 0.1), (400, 0.1)):
+        st = status()
+        out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, table, ints(lens), N, tau,
+                                        dev_status=st).cpu().numpy().reshape(-1, d)
+        assert flags(st) == 0
+        sq = np.where(q.numpy() / sigma_q.numpy()[None, :, None, None] < 0, -1, 1).reshape(-1, d)
+        for r in range(0, B * G * T, 37):
+            o, kept, bound = ocache.attend(sq[r], f.sk[0, 0], f.codes[0, 0], f.scale[0, 0],
+                                           f.zero[0, 0], N, np.float32(tau), 0, 0,
+                                           lens[r // (G * T)] - T + r % T)
+            assert (np.abs(out[r] - o) <= (kept.size / 4 + 64) * 2.0 ** -23 * bound).all(), (N, tau, r)
+
+
+@pytest.mark.parametrize("B,G,T,n", [(300, 1, 1, 11000), (1, 3, 800, 6000)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("same", [True, False])
+def test_kept_sets_over_several_segments(cache, d, B, G, T, n, same):
+    """As test_kept_sets: counts of the kept tokens of each residue, ties across segments."""
+    f = Filled(cache, [n], 1, d, 64, F32, seed=n, values=_marks, same_keys=same)
+    lens = [n - 17 * b for b in range(B)]
+    q, sigma_q = queries(B, G, T, d, F32)
+    sq = np.where(q.numpy() / sigma_q.numpy()[None, :, None, None] < 0, -1, 1).reshape(-1, d)
+    for N in (100, 3001):
+        st = status()
+        out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, f.table.repeat(B, 1),
+                                        ints(lens), N, 0.0, dev_status=st).cpu().numpy().reshape(-1, d)
+        assert flags(st) == 0
+        for r in range(0, B * G * T, 37):
+            _, kept, _ = ocache.attend(sq[r], f.sk[0, 0], f.codes[0, 0], f.scale[0, 0], f.zero[0, 0],
+                                       N, 0.0, 0, 0, lens[r // (G * T)] - T + r % T)
+            count = np.bincount(kept % d, minlength=d)
+            got = out[r] * kept.size / 15
+            assert np.array_equal(np.rint(got), count) and np.abs(got - count).max() < 0.01
+
+
+@pytest.mark.parametrize("B,G,T,n", [(300, 1, 1, 11000), (1, 3, 800, 6000)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_an_unholdable_value_in_a_later_segment(cache, d, B, G, T, n):
+    def values(b, h, t, e):
+        v = torch.ones(b, h, t, e)
+        v[0, 0, n - 200 - 17 * (B - 1), 5] = float("nan")
+        return v
+    f = Filled(cache, [n], 1, d, 64, F32, seed=n, values=values)
+    lens = [n - 17 * b for b in range(B)]
+    q, sigma_q = queries(B, G, T, d, F32)
+    sq = np.where(q.numpy() / sigma_q.numpy()[None, :, None, None] < 0, -1, 1).reshape(-1, d)
+    out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, f.table.repeat(B, 1),
+                                    ints(lens), n // 2, 0.1).cpu().numpy().reshape(-1, d)
+    nans = 0
+    for r in range(0, B * G * T, 7):
+        o, kept, bound = ocache.attend(sq[r], f.sk[0, 0], f.codes[0, 0], f.scale[0, 0], f.zero[0, 0],
+                                       n // 2, np.float32(0.1), 0, 0, lens[r // (G * T)] - T + r % T)
+        assert np.array_equal(np.isnan(out[r]), np.isnan(o))
+        nans += np.isnan(o).any()
+        if not np.isnan(o).any():
+            assert (np.abs(out[r] - o) <= (kept.size / 4 + 64) * 2.0 ** -23 * bound).all()
+    assert 0 < nans < B * G * T / 7
