@@ -493,7 +493,10 @@ HAD_API had_status_t had_cache_fork(int32_t *table, int32_t *lens, int32_t *refs
  * fresh one, src[s] -> dst[s] naming the copy that had_cache_copy_pages then
  * makes (-1: none); of the growing sequences that share it the last one keeps
  * it if no other holds it.  Pages reserved by an earlier call and not used
- * yet are kept.  lens is not changed.
+ * yet are kept, but for those that another table entry names as well (a length
+ * that the caller lowered after a fork leaves such pages behind it): they are
+ * let go for fresh ones, with nothing to copy.  A page that this call lets go
+ * is not handed out again before the next one.  lens is not changed.
  *   grow    [S] int32, >= 0;  src, dst [S] int32 out
  * Too few free pages flags HAD_ERR_NO_PAGES; a grow < 0, more than
  * max_pages * page tokens, or a table that lacks the last page flags

@@ -88,7 +88,7 @@ class Books:
         """(src, dst), or None where the pool has too few free pages."""
         keep = [list(r) for r in self.table], list(self.refs)
         free = iter([p for p, r in enumerate(self.refs) if r == 0])
-        holders = list(self.refs)
+        before, holders = list(self.refs), list(self.refs)
         src, dst = [-1] * len(grow), [-1] * len(grow)
         try:
             for s, g in enumerate(grow):
@@ -103,6 +103,8 @@ class Books:
                     row[have - 1] = dst[s]
                     self.refs[dst[s]] = 1
                 for c in range(have, want):
+                    if row[c] >= 0 and before[row[c]] > 1:      # another entry's too
+                        self._drop(s, c)
                     if row[c] < 0:
                         row[c] = next(free)
                         self.refs[row[c]] = 1

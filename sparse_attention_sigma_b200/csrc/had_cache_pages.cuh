@@ -145,14 +145,25 @@ cache_fork_kernel(Books k, const int32_t *__restrict__ src, const int32_t *__res
 // ascending order to ascending (sequence, entry).  Of the growing sequences
 // that share a last page the last one keeps it when nobody else holds it.
 //
+// Entries behind a length are kept, but for pages that another entry names as
+// well (a length that went back after a fork leaves such): those are let go for
+// fresh ones.
+//
 // Each CTA looks at an eighth of the sequences and at an eighth of refs; three
 // cluster barriers pass on what the others need: the last pages, the numbers
-// of wanted and of free pages, and that all have read the old books.
+// of wanted and of free pages, and that all have read the old books.  Rows whose
+// wanted entries are not simply the last ones take two more: an owner first
+// writes each such entry's number among the row's into the table, where the
+// thread that has the page of that number finds it.  A page that is let go
+// meanwhile carries kLetGo, so that it is seen as shared and not as free until
+// all are done.
 struct ReserveShared {
     long long wide[kBookWarps];
     int buf[kBookWarps];
-    int free_pages, bad;
+    int free_pages, bad, uneven;
 };
+
+constexpr int kLetGo = 1 << 30;        // in refs, which stay far below
 
 inline size_t reserve_smem_bytes(int seqs)
 {
@@ -165,7 +176,7 @@ cache_reserve_kernel(Books k, const int32_t *__restrict__ grow, int32_t *src, in
 {
     extern __shared__ int reserve_smem[];
     int *last = reserve_smem;              // [S] shared last page of a growing sequence, or -1
-    int *first = last + k.seqs;            // [S] first entry that gets a fresh page
+    int *first = last + k.seqs;            // [S] first entry that gets a fresh page, ~ of it in an uneven row
     int *need = first + k.seqs;            // [S] fresh pages wanted; the copy, if any, included
     int *upto = need + k.seqs;             // [S + 1] exclusive prefix of need
     __shared__ ReserveShared sh;
@@ -178,8 +189,11 @@ cache_reserve_kernel(Books k, const int32_t *__restrict__ grow, int32_t *src, in
     const int p1 = (int)((long long)k.pages * (rank + 1) / kBookCtas);
     const int page = 1 << k.page_log;
 
+    // behind the length: a page that another entry names as well
+    auto shared_behind = [&](int p) { return p < k.pages && k.refs[p] > 1; };
+
     // a warp per sequence
-    int bad = 0;
+    int bad = 0, uneven = 0;
     for (int s = s0 + warp; s < s1; s += kBookWarps) {
         const int len = k.lens[s], g = grow[s];
         int shared_page = -1, from = 0, wanted = 0;
@@ -197,18 +211,26 @@ cache_reserve_kernel(Books k, const int32_t *__restrict__ grow, int32_t *src, in
                 else if (k.refs[p] > 1)
                     shared_page = p;
             }
-            // entries already held from an earlier call come first, then free ones
+            // entries held from an earlier call come first, then those to be filled
             from = want;
-            int held_behind = 0;
+            int hole = want, held_behind = 0, odd = 0;
             for (int c0 = have; c0 < want; c0 += 32) {
                 const int p = c0 + lane < want ? row[c0 + lane] : -1;
                 if (p >= k.pages) bad = 1;
-                const unsigned none = __ballot_sync(kFullMask, p < 0 && c0 + lane < want);
-                if (none && from == want) from = c0 + __ffs(none) - 1;
-                held_behind |= p >= 0 && c0 + lane > from;
+                const bool none = p < 0 && c0 + lane < want, swap = p >= 0 && shared_behind(p);
+                const unsigned nones = __ballot_sync(kFullMask, none);
+                const unsigned fill = __ballot_sync(kFullMask, none || swap);
+                if (nones && hole == want) hole = c0 + __ffs(nones) - 1;
+                if (fill && from == want) from = c0 + __ffs(fill) - 1;
+                wanted += __popc(fill);
+                held_behind |= p >= 0 && c0 + lane > hole;
+                odd |= swap;
             }
             if (held_behind) bad = 1;
-            wanted = want - from;
+            if (__any_sync(kFullMask, odd)) {
+                uneven = 1;
+                from = ~from;
+            }
         }
         if (lane == 0) {
             last[s] = shared_page;
@@ -221,9 +243,11 @@ cache_reserve_kernel(Books k, const int32_t *__restrict__ grow, int32_t *src, in
     for (int p = p0 + tid; p < p1; p += kBookThreads) n += k.refs[p] == 0;
     n = block_sum(n, sh.buf);
     bad = __syncthreads_or(bad);
+    uneven = __syncthreads_or(uneven);
     if (tid == 0) {
         sh.free_pages = n;
         sh.bad = bad;
+        sh.uneven = uneven;
     }
     cluster.sync();
     for (int s = tid; s < k.seqs; s += kBookThreads) {
@@ -246,6 +270,7 @@ cache_reserve_kernel(Books k, const int32_t *__restrict__ grow, int32_t *src, in
         before += r < rank ? o->free_pages : 0;
         free_pages += o->free_pages;
         bad |= o->bad;
+        uneven |= o->uneven;
     }
     cluster.sync();
     for (int s = tid; s < k.seqs; s += kBookThreads) {
@@ -283,9 +308,33 @@ cache_reserve_kernel(Books k, const int32_t *__restrict__ grow, int32_t *src, in
         const bool copy = !refuse && last[s] >= 0;
         src[s] = copy ? last[s] : -1;
         if (!copy) dst[s] = -1;
-        if (copy) atomicSub(k.refs + last[s], 1);
+        if (copy) {
+            if (uneven) atomicOr(k.refs + last[s], kLetGo);
+            atomicSub(k.refs + last[s], 1);
+        }
     }
     if (refuse) return;
+    if (uneven) {                          // the same in every CTA
+        for (int s = s0 + warp; s < s1; s += kBookWarps) {
+            if (first[s] >= 0) continue;
+            int32_t *row = k.table + (long long)s * k.max_pages;
+            const int want = pages_of(k.lens[s] + grow[s], k.page_log);
+            int nth = 0;
+            for (int c0 = ~first[s]; c0 < want; c0 += 32) {
+                const int c = c0 + lane, p = c < want ? row[c] : -1;
+                const bool swap = p >= 0 && shared_behind(p);
+                if (swap) {
+                    atomicOr(k.refs + p, kLetGo);
+                    atomicSub(k.refs + p, 1);
+                }
+                const bool fill = c < want && (p < 0 || swap);
+                const unsigned fills = __ballot_sync(kFullMask, fill);
+                if (fill) row[c] = -2 - nth - __popc(fills & ((1u << lane) - 1));
+                nth += __popc(fills);
+            }
+        }
+        cluster.sync();
+    }
     // the free pages of this CTA's range to the entries of the same ranks
     for (int q0 = p0; q0 < p1 && before < total; q0 += kBookThreads) {
         const int p = q0 + tid;
@@ -306,10 +355,19 @@ cache_reserve_kernel(Books k, const int32_t *__restrict__ grow, int32_t *src, in
         if (copy && nth == 0) {
             row[pages_of(k.lens[lo], k.page_log) - 1] = p;
             dst[lo] = p;
-        } else {
+        } else if (first[lo] >= 0) {
             row[first[lo] + nth - copy] = p;
+        } else {
+            int c = ~first[lo] + nth - copy;       // or behind it, by as many entries as are kept
+            while (c < k.max_pages - 1 && row[c] != -2 - (nth - copy)) ++c;
+            row[c] = p;
         }
         k.refs[p] = 1;
+    }
+    if (uneven) {
+        cluster.sync();                    // nobody looks for free pages any more
+        for (int p = p0 + tid; p < p1; p += kBookThreads)
+            if (k.refs[p] > 0 && (k.refs[p] & kLetGo)) k.refs[p] &= ~kLetGo;
     }
 }
 

@@ -934,3 +934,96 @@ def test_an_unholdable_value_in_a_later_segment(cache, d, B, G, T, n):
         if not np.isnan(o).any():
             assert (np.abs(out[r] - o) <= (kept.size / 4 + 64) * 2.0 ** -23 * bound).all()
     assert 0 < nans < B * G * T / 7
+
+
+def _lowered(cache, S, width, P, page, seed, evict):
+    """Forks, lengths that go back and growth in turn, against the oracle."""
+    g = np.random.default_rng(seed)
+    table, lens, refs = cache.empty_books(S, width, P)
+    b = ocache.Books(table, lens, refs, page)
+    st = status()
+    exchanged = gone = 0
+    for step in range(40):
+        before = np.array(b.table), np.array(b.refs)
+        grow = g.integers(0, max(2, width * page // 3), S) * (g.random(S) < 0.7)
+        grow = np.minimum(grow, width * page - np.array(b.lens))
+        src, dst = cache.had_cache_reserve(table, lens, refs, page, ints(grow.tolist()), dev_status=st)
+        want = b.reserve(grow.tolist())
+        if want is None:
+            assert flags(st) == NO_PAGES
+            st.zero_()
+            want = [-1] * S, [-1] * S
+            all_gone = g.integers(0, S, S // 2 + 1)
+            cache.had_cache_free(table, lens, refs, ints(all_gone.tolist()), dev_status=st)
+            b.free(all_gone.tolist())
+        else:
+            lens += ints(grow.tolist())
+            b.lens = [n + int(x) for n, x in zip(b.lens, grow)]
+            now = np.array(b.table)
+            changed = (before[0] >= 0) & (now != before[0])
+            exchanged += int(changed.sum()) - sum(x >= 0 for x in want[0])
+            gone += int(((before[1] > 0) & (np.array(b.refs) == 0)).sum())
+        assert src.tolist() == want[0] and dst.tolist() == want[1]
+        _same_books(table, lens, refs, b)
+        n = int(g.integers(0, S + 1))
+        to, frm = g.permutation(S)[:n], g.integers(0, S, n)
+        cache.had_cache_fork(table, lens, refs, page, ints(frm.tolist()), ints(to.tolist()),
+                             dev_status=st)
+        b.fork(frm.tolist(), to.tolist())
+        if evict and step % 2:
+            W = int(g.integers(1, width * page))
+            cache.had_cache_evict(table, lens, refs, page, W, 0, dev_status=st)
+            b.evict(W, 0)
+        # some go back, to any length that still has its last page
+        for s in np.flatnonzero(g.random(S) < 0.5):
+            n = int(g.integers(0, b.lens[s] + 1))
+            if n % page and b.table[s][n // page] < 0:
+                n = 0
+            b.lens[s] = n
+        lens.copy_(ints(b.lens))
+        _same_books(table, lens, refs, b)
+        assert flags(st) == 0
+        counted = np.bincount(table[table >= 0].cpu().numpy(), minlength=P)
+        assert np.array_equal(counted, refs.cpu().numpy())
+    return exchanged, gone
+
+
+LOWERED = [(2, 4, 12, 16, 0), (5, 9, 60, 16, 1), (9, 40, 300, 32, 2), (64, 40, 2000, 64, 3),
+           (33, 70, 1500, 16, 4), (700, 12, 7000, 16, 5)]
+
+
+@pytest.mark.parametrize("S,width,P,page,seed", LOWERED)
+def test_books_where_lengths_go_back_after_forks(cache, S, width, P, page, seed):
+    """Pages behind a length that another sequence reads are exchanged, never written."""
+    exchanged, gone = _lowered(cache, S, width, P, page, seed, False)
+    assert exchanged >= 10 and gone > 0      # the run does what it is for
+
+
+def test_a_sequence_that_went_back_after_a_fork_leaves_the_other_as_it_was(cache):
+    H, d, page = 2, 64, 16
+    f = Filled(cache, [70], H, d, page, F32, spare=12)
+    table = torch.full((2, 8), -1, dtype=I, device="cuda")
+    table[:1, :f.table.shape[1]] = f.table
+    lens, st = ints([70, 0]), status()
+    cache.had_cache_fork(table, lens, f.refs, page, ints([0]), ints([1]), dev_status=st)
+    before = cache.had_cache_read(f.cache, table[:1], ints([0]), 70, dev_status=st)
+    k, v = torch.randn(2, H, 60, d, device="cuda"), torch.randn(2, H, 60, d, device="cuda")
+    for back in (48, 37, 16, 0):
+        lens[1] = back
+        grow = ints([0, 50])
+        src, dst = cache.had_cache_reserve(table, lens, f.refs, page, grow, dev_status=st)
+        cache.had_cache_copy_pages(f.cache, src, dst, dev_status=st)
+        cache.had_cache_append(k, v, f.sigma.cuda(), f.cache, table, lens, counts=grow, dev_status=st)
+        lens += grow
+        after = cache.had_cache_read(f.cache, table[:1], ints([0]), 70, dev_status=st)
+        assert flags(st) == 0
+        assert torch.equal(before[0], after[0]) and torch.equal(before[1], after[1])
+        # the other one has the common tokens and its own
+        bits, values = cache.had_cache_read(f.cache, table[1:], ints([0]), back + 50, dev_status=st)
+        assert torch.equal(bits[:, :, :back], before[0][:, :, :back])
+        assert torch.equal(values[:, :, :back], before[1][:, :, :back])
+        code, s, z = ocache.quantise(v[1:, :, :50].cpu().numpy())
+        own = (code * s[..., None].astype(np.float64) + z[..., None]).astype(np.float32)
+        assert np.array_equal(values[:, :, back:].cpu().numpy(), own)
+        counted = np.bincount(table[table >= 0].cpu().numpy(), minlength=f.refs.numel())
+        assert np.array_equal(counted, f.refs.cpu().numpy())

@@ -303,3 +303,26 @@ def test_books_by_hand():
     assert b.table == [[-1, -1, 0, -1], [-1, -1, 1, -1]] and b.refs == [1, 1, 0, 0, 0, 0]
     b.free([1, 1])
     assert b.table[1] == [-1] * 4 and b.lens == [33, 0] and b.refs == [1, 0, 0, 0, 0, 0]
+
+
+def test_books_by_hand_where_a_length_was_lowered():
+    # 20 tokens in pages 0 and 1, forked; the copy goes back to 16 tokens and on by 4: page 1,
+    # behind its length, is the other one's too
+    b = ocache.Books([[0, 1, -1], [-1] * 3], [20, 0], [1, 1, 0, 0, 0], 16)
+    b.fork([0], [1])
+    b.lens[1] = 16
+    assert b.reserve([0, 4]) == ([-1, -1], [-1, -1])
+    assert b.table == [[0, 1, -1], [0, 2, -1]] and b.refs == [2, 1, 1, 0, 0]
+    # both go back to 10 tokens and on: page 0 is copied for the first, and kept by the last
+    b.lens = [10, 10]
+    assert b.reserve([1, 1]) == ([0, -1], [3, -1])
+    assert b.table == [[3, 1, -1], [0, 2, -1]] and b.refs == [1, 1, 1, 1, 0]
+    # three hold page 1 behind their lengths: whoever grows over it lets it go
+    b = ocache.Books([[0, 1], [2, 1], [3, 1]], [16, 16, 16], [1, 3, 1, 1, 0, 0, 0], 16)
+    assert b.reserve([1, 0, 5]) == ([-1] * 3, [-1] * 3)
+    assert b.table == [[0, 4], [2, 1], [3, 5]] and b.refs == [1, 1, 1, 1, 1, 1, 0]
+    # a page that all let go is free for the next call
+    b = ocache.Books([[0, 1], [2, 1]], [16, 16], [1, 2, 1, 0, 0], 16)
+    assert b.reserve([1, 1]) == ([-1] * 2, [-1] * 2)
+    assert b.table == [[0, 3], [2, 4]] and b.refs == [1, 0, 1, 1, 1]
+    assert ocache.Books([[0, 1], [2, 1]], [16, 16], [1, 2, 1, 0], 16).reserve([1, 1]) is None
