@@ -495,8 +495,10 @@ HAD_API had_status_t had_cache_fork(int32_t *table, int32_t *lens, int32_t *refs
  * it if no other holds it.  Pages reserved by an earlier call and not used
  * yet are kept, but for those that another table entry names as well (a length
  * that the caller lowered after a fork leaves such pages behind it): they are
- * let go for fresh ones, with nothing to copy.  A page that this call lets go
- * is not handed out again before the next one.  lens is not changed.
+ * let go for fresh ones, with nothing to copy.  Entries that are missing before
+ * kept ones (evicted pages of a sequence that starts again) are filled where
+ * they stand.  A page that this call lets go is not handed out again before the
+ * next one.  lens is not changed.
  *   grow    [S] int32, >= 0;  src, dst [S] int32 out
  * Too few free pages flags HAD_ERR_NO_PAGES; a grow < 0, more than
  * max_pages * page tokens, or a table that lacks the last page flags

@@ -147,7 +147,7 @@ cache_fork_kernel(Books k, const int32_t *__restrict__ src, const int32_t *__res
 //
 // Entries behind a length are kept, but for pages that another entry names as
 // well (a length that went back after a fork leaves such): those are let go for
-// fresh ones.
+// fresh ones.  Missing entries are filled where they stand.
 //
 // Each CTA looks at an eighth of the sequences and at an eighth of refs; three
 // cluster barriers pass on what the others need: the last pages, the numbers
@@ -211,22 +211,18 @@ cache_reserve_kernel(Books k, const int32_t *__restrict__ grow, int32_t *src, in
                 else if (k.refs[p] > 1)
                     shared_page = p;
             }
-            // entries held from an earlier call come first, then those to be filled
+            // entries held from an earlier call come first, as a rule, then those to be filled
             from = want;
-            int hole = want, held_behind = 0, odd = 0;
+            int odd = 0;
             for (int c0 = have; c0 < want; c0 += 32) {
                 const int p = c0 + lane < want ? row[c0 + lane] : -1;
                 if (p >= k.pages) bad = 1;
                 const bool none = p < 0 && c0 + lane < want, swap = p >= 0 && shared_behind(p);
-                const unsigned nones = __ballot_sync(kFullMask, none);
                 const unsigned fill = __ballot_sync(kFullMask, none || swap);
-                if (nones && hole == want) hole = c0 + __ffs(nones) - 1;
                 if (fill && from == want) from = c0 + __ffs(fill) - 1;
                 wanted += __popc(fill);
-                held_behind |= p >= 0 && c0 + lane > hole;
-                odd |= swap;
+                odd |= p >= 0 && (swap || c0 + lane > from);
             }
-            if (held_behind) bad = 1;
             if (__any_sync(kFullMask, odd)) {
                 uneven = 1;
                 from = ~from;

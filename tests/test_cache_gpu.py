@@ -1027,3 +1027,17 @@ def test_a_sequence_that_went_back_after_a_fork_leaves_the_other_as_it_was(cache
         assert np.array_equal(values[:, :, back:].cpu().numpy(), own)
         counted = np.bincount(table[table >= 0].cpu().numpy(), minlength=f.refs.numel())
         assert np.array_equal(counted, f.refs.cpu().numpy())
+
+
+@pytest.mark.parametrize("S,width,P,page,seed", LOWERED)
+def test_books_where_lengths_go_back_over_evicted_pages(cache, S, width, P, page, seed):
+    """Entries behind a length may be missing before others that are there."""
+    _lowered(cache, S, width, P, page, seed, True)
+
+
+def test_a_sequence_that_starts_again_over_evicted_pages(cache):
+    page, st = 16, status()
+    table, lens, refs = ints([[-1, -1, 4, -1, 2]]), ints([0]), ints([0, 0, 1, 0, 1, 0, 0])
+    src, dst = cache.had_cache_reserve(table, lens, refs, page, ints([80]), dev_status=st)
+    assert flags(st) == 0 and src.tolist() == dst.tolist() == [-1]
+    assert table.tolist() == [[0, 1, 4, 3, 2]] and refs.tolist() == [1, 1, 1, 1, 1, 0, 0]

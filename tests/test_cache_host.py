@@ -326,3 +326,11 @@ def test_books_by_hand_where_a_length_was_lowered():
     assert b.reserve([1, 1]) == ([-1] * 2, [-1] * 2)
     assert b.table == [[0, 3], [2, 4]] and b.refs == [1, 0, 1, 1, 1]
     assert ocache.Books([[0, 1], [2, 1]], [16, 16], [1, 2, 1, 0], 16).reserve([1, 1]) is None
+
+
+def test_books_by_hand_where_entries_are_missing_behind_the_length():
+    # a sequence whose first pages were let go starts again: the holes are filled where they are
+    b = ocache.Books([[-1, -1, 4, -1, 2]], [70], [0, 0, 1, 0, 1, 0, 0], 16)
+    b.lens = [0]
+    assert b.reserve([80]) == ([-1], [-1])
+    assert b.table == [[0, 1, 4, 3, 2]] and b.refs == [1, 1, 1, 1, 1, 0, 0]
