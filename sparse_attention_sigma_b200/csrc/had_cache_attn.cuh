@@ -27,10 +27,11 @@
 //      core.  The codes are whole numbers below 16, exact in fp16; the weights
 //      p s are fp32, brought into fp16's range by a power of two per row that
 //      only comes down when a larger weight appears, and cut into two fp16
-//      terms (24 bits, down to 2^-36 of the row's largest weight), stacked as
-//      rows of A: row x = 8 term + r.  So the product is as exact as fp32 for
-//      scales of any size.  It takes c - 8 in place of c; the rest, p (z + 8 s),
-//      is summed beside it.
+//      terms, stacked as rows of A: row x = 8 term + r.  The terms are off by
+//      2^-23 of their weight at most, or by 2^-37 of the row's largest weight
+//      p s, for scales of any size.  The product takes c - 8 in place of c; the
+//      rest, p (z + 8 s), is summed beside it, so an element's error is measured
+//      by sum p (8 s + |z + 8 s|): far below the values' own step s.
 //   5. Warps, terms and CTAs are added in a fixed order.
 // The union of the rows' kept keys is read once, each key's bits once.
 //
@@ -233,7 +234,6 @@ struct CacheAttnShared {
         float part[RM][D];             // at the end: this CTA's sums
     };
     int level[RM], quota[RM];
-    float top[RM];                     // the largest weight p
     int ranked;                        // some row keeps only part of its ties
     int ties[kCacheAttnWarps][RM];
     float zsum[kCacheAttnWarps][RM];
@@ -553,7 +553,6 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
             if (lane * EL + e <= D + 1) sh.p[r][lane * EL + e] = lane * EL + e <= D ? w[e] * inv : 0.0f;
         if (lane == 0) {
             sh.level[r] = level;
-            sh.top[r] = inv;
             if (level < 0) sh.quota[r] = 0;
         }
     }
@@ -717,7 +716,8 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         // The same where a scale is NaN or a weight passes fp16's range: the rows'
-        // scales come down so that the largest weight of the chunk is below 2^13,
+        // scales come down so that the largest weight of the chunk is below 2^13
+        // (four times more may come before the next time),
         // and p z is summed again with what is kept alone.
         auto reweigh = [&](int c, float (&v_a)[RW], float (&v_b)[RW], const float (&zkeep)[RW]) -> bool {
             const int pair = lane & 7, sub = lane >> 3;
@@ -733,8 +733,10 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                 const float p_a = sh.p[r][h_a], p_b = sh.p[r][h_b];
                 const float w_a = h_a == kUnseen ? 0.0f : p_a * s_a, w_b = h_b == kUnseen ? 0.0f : p_b * s_b;
                 zacc[i] = zkeep[i] + ((h_a == kUnseen ? 0.0f : p_a * z_a) + (h_b == kUnseen ? 0.0f : p_b * z_b));
-                // the most that keys of these scales can weigh (NaN is no number to scale by)
-                float most = fmaxf(h_a == kUnseen ? 0.0f : sh.top[r] * s_a, h_b == kUnseen ? 0.0f : sh.top[r] * s_b);
+                // the chunk's largest weight, and not the largest that its scales allow: a key
+                // of a huge scale and no weight would take the others' bits (NaN is no number
+                // to scale by)
+                float most = fmaxf(w_a, w_b);
 #pragma unroll
                 for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(kFullMask, most, o));
                 // 2^12 <= most 2^(12 - e) < 2^13, with e >= -115

@@ -1041,3 +1041,46 @@ def test_a_sequence_that_starts_again_over_evicted_pages(cache):
     src, dst = cache.had_cache_reserve(table, lens, refs, page, ints([80]), dev_status=st)
     assert flags(st) == 0 and src.tolist() == dst.tolist() == [-1]
     assert table.tolist() == [[0, 1, 4, 3, 2]] and refs.tolist() == [1, 1, 1, 1, 1, 0, 0]
+
+
+@pytest.mark.parametrize("G,d,n", [(1, 64, 31), (1, 128, 400), (3, 64, 400), (4, 128, 3000)])
+def test_large_values_of_keys_that_weigh_little(cache, G, d, n):
+    """Scales that make up for the weights: every kept token adds as much to the first row.  exp's
+    argument goes up to 65, in place of the 23 of the bound, so that takes three times its units."""
+    tau = 2.0
+    f = Filled(cache, [n], 1, d, 64, F32, seed=n)
+    q, sigma_q = queries(1, G, 1, d, F32)
+    sq = np.where(q.numpy() / sigma_q.numpy()[None, :, None, None] < 0, -1, 1)
+    logit = tau * (f.sk[0, 0] @ sq[0, 0, 0])
+    size = torch.from_numpy(np.exp(np.minimum(logit.max() - logit, 64.0)))
+    v = (torch.randn(1, 1, n, d, generator=torch.Generator().manual_seed(3)) * size[:, None]).float()
+    f = Filled(cache, [n], 1, d, 64, F32, seed=n, values=lambda *_: v)
+    st = status()
+    out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, f.table, ints([n]), n, tau,
+                                    dev_status=st)
+    assert flags(st) == 0
+    want, bound = f.rows(q, sigma_q, [n], [1], n, tau, 0, 0)
+    assert (np.abs(out.cpu().numpy() - want) <= 3 * bound).all()
+
+
+@pytest.mark.parametrize("ratio", [24, 30, 36, 40, 90])
+@pytest.mark.parametrize("at", [5, 20])
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_huge_value_that_weighs_next_to_nothing(cache, d, at, ratio):
+    """31 tokens equal to the query and one opposite to it, of weight e^-69 = 1e-30, whose scale is
+    2^ratio times theirs."""
+    n = 32
+    f = Filled(cache, [n], 1, d, 32, F32, same_keys=True)
+    k = f.k.clone()
+    k[:, :, at] = -k[:, :, at]
+    v = torch.randn(1, 1, n, d, generator=torch.Generator().manual_seed(1))
+    v[:, :, at] *= 2.0 ** ratio
+    st, tau = status(), 34.5 / d
+    cache.had_cache_append(k.cuda(), v.cuda(), f.sigma.cuda(), f.cache, f.table, ints([0]), dev_status=st)
+    out = cache.had_cache_attention(f.k[:, :, :1].contiguous().cuda(), f.sigma.cuda(), f.cache, f.table,
+                                    ints([n]), n, tau, dev_status=st)
+    assert flags(st) == 0
+    f.sk[:, :, at] *= -1
+    f.codes, f.scale, f.zero = ocache.quantise(v.numpy())
+    want, bound = f.rows(f.k[:, :, :1], f.sigma, [n], [1], n, tau, 0, 0)
+    assert (np.abs(out.cpu().numpy() - want) <= bound).all()
