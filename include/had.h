@@ -394,7 +394,8 @@ HAD_API size_t had_noalloc_scratch_bytes(void);
  *     kbits   [pages, heads, page, d/32] uint32 (device), packed as above
  *     vcodes  [pages, heads, page, d/2] uint8: element 2i of the value in the
  *             low nibble of byte i, element 2i + 1 in the high one
- *     vscale  [pages, heads, page, 2] bf16: s, then z
+ *     vscale  [pages, heads, page, 2] bf16: s, then z.  s of either sign, both
+ *             finite and c s + z within fp32 for every c, or both NaN
  *     page    16, 32, 64, 128 or 256;  d 64 or 128
  *     pages * heads * page < 2^32;  pages < 2^31 - 2^16
  *   table   [S, max_pages] int32 (device): pages of sequence s in order, -1

@@ -736,7 +736,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                 // the chunk's largest weight, and not the largest that its scales allow: a key
                 // of a huge scale and no weight would take the others' bits (NaN is no number
                 // to scale by)
-                float most = fmaxf(w_a, w_b);
+                float most = fmaxf(fabsf(w_a), fabsf(w_b));
 #pragma unroll
                 for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(kFullMask, most, o));
                 // 2^12 <= most 2^(12 - e) < 2^13, with e >= -115
@@ -777,7 +777,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                 v_b[i] = p_b * scale[i] * s_b;
                 zkeep[i] = zacc[i];
                 zacc[i] = fmaf(p_a, z_a, fmaf(p_b, z_b, zacc[i]));
-                odd = odd || fmaxf(v_a[i], v_b[i]) > kMostWeight;
+                odd = odd || fmaxf(fabsf(v_a[i]), fabsf(v_b[i])) > kMostWeight;   // s of either sign
             }
             bool changed = false;
             if (__builtin_expect(__any_sync(kFullMask, odd), 0)) changed = reweigh(c, v_a, v_b, zkeep);

@@ -1084,3 +1084,30 @@ def test_one_huge_value_that_weighs_next_to_nothing(cache, d, at, ratio):
     f.codes, f.scale, f.zero = ocache.quantise(v.numpy())
     want, bound = f.rows(f.k[:, :, :1], f.sigma, [n], [1], n, tau, 0, 0)
     assert (np.abs(out.cpu().numpy() - want) <= bound).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales_of_either_sign(cache, d):
+    """A pool that append did not write: c s + z with negative and zero scales of any size."""
+    n = 500
+    f = Filled(cache, [n], 2, d, 16, F32, seed=6)
+    g = torch.Generator().manual_seed(7)
+    scale = torch.randn(f.cache.vscale.shape, generator=g)
+    scale = scale * 10.0 ** torch.randint(-20, 21, scale.shape[:3] + (1,), generator=g)
+    scale[torch.rand(scale.shape[:3], generator=g) < 0.1, 0] = 0.0
+    f.cache.vscale.copy_(scale)
+    pages = f.table[0, :-(-n // 16)].cpu().long()
+    sz = scale.bfloat16().double()[pages].permute(1, 0, 2, 3).reshape(2, -1, 2)[:, :n].numpy()
+    f.scale, f.zero = sz[None, ..., 0], sz[None, ..., 1]
+    q, sigma_q = queries(1, 6, 1, d, F32)
+    for N in (20, n):
+        st = status()
+        out = cache.had_cache_attention(q.cuda(), sigma_q.cuda(), f.cache, f.table, ints([n]), N, 0.1,
+                                        dev_status=st)
+        assert flags(st) == 0
+        want, _ = f.rows(q, sigma_q, [n], [1], N, 0.1, 0, 0)
+        # what is summed is p (c - 8) s and p (z + 8 s): 16 steps and z at most
+        codes, f.codes = f.codes, np.full_like(f.codes, 16)
+        _, bound = f.rows(q, sigma_q, [n], [1], N, 0.1, 0, 0)
+        f.codes = codes
+        assert (np.abs(out.cpu().numpy() - want) <= bound).all()
