@@ -83,16 +83,19 @@ had_status_t check_books(int32_t *table, const int32_t *lens, int32_t *refs, int
     return s;
 }
 
-// A launch in clusters of `ctas` CTAs.
+// A launch in clusters of `ctas` CTAs.  `most_smem`: the most that any launch of
+// this kernel takes; the limit is set to that and never to less, since host
+// threads that launch it at once share it.
 template <typename... Params, typename... Args>
 had_status_t launch_clusters(void (*kernel)(Params...), unsigned grid, unsigned ctas,
-                             unsigned threads, size_t smem, cudaStream_t st, Args... args)
+                             unsigned threads, size_t smem, size_t most_smem, cudaStream_t st,
+                             Args... args)
 {
     // 48 KB, the kernel's own variables included, need no attribute.  Set on
     // every call: it belongs to the current device.
     if (smem > 24 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-            cudaSuccess)
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)most_smem) != cudaSuccess)
         return failed();
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -110,11 +113,17 @@ had_status_t launch_clusters(void (*kernel)(Params...), unsigned grid, unsigned 
 
 // A launch of one cluster of the page operators.
 template <typename... Params, typename... Args>
-had_status_t launch_cluster(void (*kernel)(Params...), size_t smem, cudaStream_t st, Args... args)
+had_status_t launch_cluster(void (*kernel)(Params...), size_t smem, size_t most_smem,
+                            cudaStream_t st, Args... args)
 {
-    return launch_clusters(kernel, had::kBookCtas, had::kBookCtas, had::kBookThreads, smem, st,
-                           args...);
+    return launch_clusters(kernel, had::kBookCtas, had::kBookCtas, had::kBookThreads, smem,
+                           most_smem, st, args...);
 }
+
+// Keys that a CTA holds at once at most: 20 KB of distances, so that four CTAs
+// (three at d 128 with eight rows) share an SM.
+template <int RW>
+constexpr int kMostKeys = 20 * 1024 / (4 * RW) / 128 * 128;
 
 template <int D, int RW, bool kLong>
 had_status_t launch_attention_plan(const had::CacheAttnArgs &a, long long tiles,
@@ -128,7 +137,8 @@ had_status_t launch_attention_plan(const had::CacheAttnArgs &a, long long tiles,
     plan.by_group = had::divisor((unsigned)(a.Hq / a.c.heads));
     return launch_clusters(had::cache_attn_kernel<D, RW, kLong>, (unsigned)(tiles * plan.ctas),
                            (unsigned)plan.ctas, kThreads,
-                           had::cache_attn_smem_bytes<D, RW>(plan.cap), st, a, plan);
+                           had::cache_attn_smem_bytes<D, RW>(plan.cap),
+                           had::cache_attn_smem_bytes<D, RW>(kMostKeys<RW>), st, a, plan);
 }
 
 template <int D, int RW>
@@ -147,8 +157,7 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, int max_l
         keys = seen < keys ? seen : keys;
     }
     const long long tiles = (long long)B * a.c.heads * plan.tiles;
-    // 20 KB of distances at once, so that four CTAs share an SM
-    constexpr long long most = 20 * 1024 / (4 * RW) / 128 * 128;
+    constexpr long long most = kMostKeys<RW>;
     // CTAs until four per SM are busy, each with 512 keys or more; the device uses
     // fewer for a tile that has fewer keys.  Measured with 1, 2, 4 and 8: 64 tiles
     // of 4 k keys 38, 23, 15.0, 15.2 us; 128 of 16 k 211, 129, 67, 73 us; 256 of
@@ -312,8 +321,8 @@ had_status_t had_cache_fork(int32_t *table, int32_t *lens, int32_t *refs, int S,
     // whole 128-byte lines of a row per tile while shared memory holds them
     int tile = 32;
     while (tile > 1 && had::fork_smem_bytes(n, S, tile) > (size_t)kMaxSmem) --tile;
-    return launch_cluster(had::cache_fork_kernel, had::fork_smem_bytes(n, S, tile), stream, k, src,
-                          dst, n, tile, dev_status);
+    return launch_cluster(had::cache_fork_kernel, had::fork_smem_bytes(n, S, tile), kMaxSmem, stream,
+                          k, src, dst, n, tile, dev_status);
 }
 
 had_status_t had_cache_reserve(int32_t *table, const int32_t *lens, int32_t *refs, int S,
@@ -328,8 +337,9 @@ had_status_t had_cache_reserve(int32_t *table, const int32_t *lens, int32_t *ref
     if (S > had::kMaxSeqs) return HAD_ERR_UNSUPPORTED;
     if (!good(grow, 4) || !good(src, 4) || !good(dst, 4) || !aligned(dev_status, 4))
         return HAD_ERR_INVALID_ARG;
-    return launch_cluster(had::cache_reserve_kernel, had::reserve_smem_bytes(S), stream, k, grow,
-                          src, dst, dev_status);
+    return launch_cluster(had::cache_reserve_kernel, had::reserve_smem_bytes(S),
+                          had::reserve_smem_bytes(had::kMaxSeqs), stream, k, grow, src, dst,
+                          dev_status);
 }
 
 had_status_t had_cache_free(int32_t *table, int32_t *lens, int32_t *refs, int S, int max_pages,
@@ -370,7 +380,7 @@ had_status_t had_cache_compact(int32_t *table, int32_t *refs, int S, int max_pag
     if (s != HAD_OK) return s;
     if (!good(src, 4) || !good(dst, 4) || !good(live, 4) || !aligned(dev_status, 4))
         return HAD_ERR_INVALID_ARG;
-    return launch_cluster(had::cache_compact_kernel, 0, stream, k, src, dst, live, dev_status);
+    return launch_cluster(had::cache_compact_kernel, 0, 0, stream, k, src, dst, live, dev_status);
 }
 
 had_status_t had_cache_copy_pages(const had_cache_t *cache, const int32_t *src,

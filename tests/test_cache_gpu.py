@@ -1111,3 +1111,68 @@ def test_scales_of_either_sign(cache, d):
         _, bound = f.rows(q, sigma_q, [n], [1], N, 0.1, 0, 0)
         f.codes = codes
         assert (np.abs(out.cpu().numpy() - want) <= bound).all()
+
+
+def _library():
+    """The C ABI itself: ctypes lets go of Python's lock during a call."""
+    import ctypes
+    from sparse_attention_sigma_b200 import build
+    lib = ctypes.CDLL(build.LIB)
+    vp, i32 = ctypes.c_void_p, ctypes.c_int
+    lib.had_cache_attention.argtypes = ([vp, i32, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32,
+                                         ctypes.c_float, i32, i32, i32, vp, vp, vp])
+    lib.had_cache_read.argtypes = [vp, vp, i32, vp, vp, i32, i32, vp, vp, vp, vp]
+    lib.had_cache_reserve.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+    return lib
+
+
+class _PoolStruct:
+    """had_cache_t of a Cache, as ctypes passes it."""
+    def __new__(cls, c):
+        import ctypes
+
+        class had_cache_t(ctypes.Structure):
+            _fields_ = [(n, ctypes.c_void_p) for n in ("kbits", "vcodes", "vscale")] + [
+                (n, ctypes.c_int) for n in ("pages", "heads", "page", "d")]
+        return ctypes.pointer(had_cache_t(c.kbits.data_ptr(), c.vcodes.data_ptr(), c.vscale.data_ptr(),
+                                          c.pages, c.heads, c.page, c.d))
+
+
+def test_host_threads_that_call_at_once(cache):
+    """Two threads whose calls take different amounts of shared memory of the same kernels."""
+    import threading
+    lib = _library()
+    H, G, d, page = 2, 2, 128, 16
+    f = Filled(cache, [1500], H, d, page, F32)
+    pool = _PoolStruct(f.cache)
+    q, sigma_q = (x.cuda() for x in queries(1, G * H, 1, d, F32))
+    lens, bad = ints([1500]), []
+    want = cache.had_cache_attention(q, sigma_q, f.cache, f.table, lens, 50, 0.1)
+    calls, keep = [], []
+    for width, S in ((1200, 1800), (2500, 8192)):               # 40 and 50 KB, 29 and 131 KB
+        table = torch.full((1, width), -1, dtype=I, device="cuda")
+        table[:, :f.table.shape[1]] = f.table
+        out, s = torch.zeros_like(want), torch.cuda.Stream()
+        books = cache.empty_books(S, 1, 10) + tuple(torch.zeros(S, dtype=I, device="cuda") for _ in "gsd")
+        keep.append((table, books, s, out))
+        t, n, r, grow, src, dst = (x.data_ptr() for x in books)
+        calls.append((
+            (q.data_ptr(), 1, sigma_q.data_ptr(), pool, table.data_ptr(), width, lens.data_ptr(), None, 1,
+             G * H, 1, 50, 0.1, 0, 0, 0, out.data_ptr(), None, s.cuda_stream),
+            (t, n, r, S, 1, 10, page, grow, src, dst, None, s.cuda_stream)))
+    torch.cuda.synchronize()
+
+    def work(attention, reserve):
+        for _ in range(400):
+            bad.extend(x for x in [lib.had_cache_attention(*attention) for _ in range(10)] if x)
+            bad.extend(x for x in [lib.had_cache_reserve(*reserve) for _ in range(10)] if x)
+
+    threads = [threading.Thread(target=work, args=c) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad, (len(bad), bad[:5])
+    for _, _, _, out in keep:
+        assert torch.allclose(out, want, rtol=1e-5, atol=1e-5)
