@@ -242,7 +242,7 @@ cache_append_kernel(const T *__restrict__ K, const T *__restrict__ V,
     constexpr int E = D / kCacheLanes, kPerWord = 32 / E;
     const int l = threadIdx.x & (kCacheLanes - 1);
     const unsigned step = gridDim.x * (256u / kCacheLanes);
-    const unsigned row0 = (blockIdx.x * 256u + threadIdx.x) / kCacheLanes;
+    const unsigned row0 = blockIdx.x * (256u / kCacheLanes) + threadIdx.x / kCacheLanes;    // (threads pass 2^32)
     CacheSlice<T, E> key[kCacheRows], value[kCacheRows];
     CacheToken token[kCacheRows];
     uint32_t at[kCacheRows];
@@ -343,7 +343,7 @@ cache_read_kernel(CacheView c, CacheTokens k, uint32_t *__restrict__ bits,
     constexpr int E = D / kReadLanes;
     const int l = threadIdx.x & (kReadLanes - 1);
     const unsigned step = gridDim.x * (256u / kReadLanes);
-    const unsigned row0 = (blockIdx.x * 256u + threadIdx.x) / kReadLanes;
+    const unsigned row0 = blockIdx.x * (256u / kReadLanes) + threadIdx.x / kReadLanes;    // (threads pass 2^32)
     uint32_t at[kReadRows];
     uint32_t codes[kReadRows][E / 4], sz[kReadRows], word[kReadRows];
 #pragma unroll

@@ -1176,3 +1176,19 @@ def test_host_threads_that_call_at_once(cache):
     assert not bad, (len(bad), bad[:5])
     for _, _, _, out in keep:
         assert torch.allclose(out, want, rtol=1e-5, atol=1e-5)
+
+
+def test_more_than_2_to_30_rows(cache):
+    """Rows of a read whose threads, eight each, pass 2^32: 4 M sequences that share one page."""
+    page, d, B = 256, 64, 2 ** 22 + 5
+    f = Filled(cache, [page], 1, d, page, F32, spare=0)
+    table = f.table[:, :1].repeat(B, 1)
+    start, st = torch.zeros(B, dtype=I, device="cuda"), status()
+    bits = torch.full((B, page, d // 32), 0x5a5a5a5a, dtype=I, device="cuda")
+    assert _library().had_cache_read(_PoolStruct(f.cache), table.data_ptr(), 1, start.data_ptr(), None, B,
+                                     page, bits.data_ptr(), None, st.data_ptr(),
+                                     torch.cuda.current_stream().cuda_stream) == 0
+    want = cache.had_cache_read(f.cache, f.table, ints([0]), page)[0][0, 0]
+    assert flags(st) == 0
+    for b in range(0, B, 1 << 19):
+        assert (bits[b:b + (1 << 19)] == want).all()
