@@ -402,7 +402,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                         qb[0] = x.x; qb[1] = x.y; qb[2] = x.z; qb[3] = x.w;
                     }
                     const int pos = mixed ? sh.pos[r] : 0, row_lo = mixed ? sh.lo[r] : 0;
-                    const int unit = 1 << (8 * (r & 3));
+                    const unsigned unit = 1u << (8 * (r & 3));
 #pragma unroll
                     for (int i = 0; i < KU; ++i) {
                         if (k0 + 32 * i >= we) break;
@@ -415,7 +415,7 @@ cache_attn_kernel(CacheAttnArgs a, CacheAttnPlan plan)
                             vis = vis && key <= pos && (key >= row_lo || key < a.sinks);
                         }
                         n = vis ? n : (int)kUnseen;
-                        word[i] += (n - (int)kUnseen) * unit;
+                        word[i] += ((unsigned)n - kUnseen) * unit;
                         if (with_hist) atomicAdd(&stage.hist[r][n], 1);
                     }
                 }

@@ -1192,3 +1192,20 @@ def test_more_than_2_to_30_rows(cache):
     assert flags(st) == 0
     for b in range(0, B, 1 << 19):
         assert (bits[b:b + (1 << 19)] == want).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_equal_and_opposite_to_keys(cache, d):
+    """Distances 0 and d in each place of a word of four: each query is a token or its opposite."""
+    n, T = 40, 8
+    f = Filled(cache, [n], 1, d, 16, F32, seed=3)
+    at = torch.tensor([0, 7, 15, 16, 31, 1, 20, 30])
+    q = f.k[:, :, at].contiguous()
+    for N in (1, n):
+        st = status()
+        for sign in (1, -1):
+            out = cache.had_cache_attention((sign * q).cuda(), f.sigma.cuda(), f.cache, f.table, ints([n]),
+                                            N, 0.1, dev_status=st)
+            want, bound = f.rows(sign * q, f.sigma, [n], [T], N, 0.1, 0, 0)
+            assert (np.abs(out.cpu().numpy() - want) <= bound).all()
+        assert flags(st) == 0
