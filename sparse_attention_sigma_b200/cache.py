@@ -82,12 +82,24 @@ def _call(function, where, args, stream, tensor):
 class Cache:
     """A pool of pages: kbits [pages, heads, page, d/32] int32, vcodes
     [pages, heads, page, d/2] uint8, vscale [pages, heads, page, 2] bfloat16.
-    Holds the tensors; a program keeps one per layer."""
-    __slots__ = ("kbits", "vcodes", "vscale", "pages", "heads", "page", "d", "_pool")
+    Holds the tensors; a program keeps one per layer, and makes another for other tensors."""
+    __slots__ = ("_tensors", "pages", "heads", "page", "d", "_pool")
 
     def __init__(self, kbits, vcodes, vscale):
         self._pool, self.pages, self.heads, self.page, self.d = _native.pool(kbits, vcodes, vscale)
-        self.kbits, self.vcodes, self.vscale = kbits, vcodes, vscale
+        self._tensors = kbits, vcodes, vscale
+
+    @property
+    def kbits(self):
+        return self._tensors[0]
+
+    @property
+    def vcodes(self):
+        return self._tensors[1]
+
+    @property
+    def vscale(self):
+        return self._tensors[2]
 
     @property
     def device(self):

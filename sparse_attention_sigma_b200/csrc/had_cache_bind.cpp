@@ -157,10 +157,26 @@ void drop_pool(PyObject *capsule)
     delete static_cast<Pool *>(PyCapsule_GetPointer(capsule, kPoolName));
 }
 
+// The address of one of a pool's tensors now: a program may give a tensor other storage.
+void *address(const Tensor &t, ScalarType type, at::IntArrayRef shape, int device)
+{
+    if (!t.is_cuda() || t.get_device() != device || t.scalar_type() != type || t.sizes() != shape ||
+        !t.is_contiguous())
+        value_error("a tensor of the cache is not what the cache was made of any more");
+    return t.data_ptr();
+}
+
 const Pool &pool_of(PyObject *o)
 {
     if (!PyCapsule_IsValid(o, kPoolName)) type_error("cache must be a Cache");
-    return *static_cast<Pool *>(PyCapsule_GetPointer(o, kPoolName));
+    Pool &p = *static_cast<Pool *>(PyCapsule_GetPointer(o, kPoolName));
+    had_cache_t &c = p.c;
+    c.kbits = static_cast<uint32_t *>(
+        address(p.kbits, ScalarType::Int, {c.pages, c.heads, c.page, c.d / 32}, p.device));
+    c.vcodes = static_cast<uint8_t *>(
+        address(p.vcodes, ScalarType::Byte, {c.pages, c.heads, c.page, c.d / 2}, p.device));
+    c.vscale = address(p.vscale, ScalarType::BFloat16, {c.pages, c.heads, c.page, 2}, p.device);
+    return p;
 }
 
 PyObject *status_of(had_status_t s) { return PyLong_FromLong((long)s); }

@@ -1209,3 +1209,27 @@ def test_queries_equal_and_opposite_to_keys(cache, d):
             want, bound = f.rows(sign * q, f.sigma, [n], [T], N, 0.1, 0, 0)
             assert (np.abs(out.cpu().numpy() - want) <= bound).all()
         assert flags(st) == 0
+
+
+def test_a_cache_whose_tensors_get_other_storage(cache):
+    """A call reads the tensors as they are: other storage of the same shape, or a refusal."""
+    f = Filled(cache, [112], 2, 64, 16, F32)
+    q, sigma_q = (x.cuda() for x in queries(1, 2, 1, 64, F32))
+    run = lambda c: cache.had_cache_attention(q, sigma_q, c, f.table, ints([112]), 9, 0.1)  # noqa: E731
+    other = [f.cache.kbits.flip(1), f.cache.vcodes.flip(1), f.cache.vscale.flip(1)]
+    want = run(cache.Cache(*other))
+    assert not torch.equal(run(f.cache), want)
+    for name, t in zip(("kbits", "vcodes", "vscale"), other):
+        with pytest.raises(AttributeError):
+            setattr(f.cache, name, t)
+        getattr(f.cache, name).data = t
+    assert torch.equal(run(f.cache), want)
+    f.cache.vcodes.data = other[1][:-1]
+    with pytest.raises(ValueError, match="any more"):
+        run(f.cache)
+    f.cache.vcodes.data = other[1].transpose(0, 1)
+    with pytest.raises(ValueError, match="any more"):
+        cache.had_cache_copy_pages(f.cache, ints([0]), ints([1]))
+    f.cache.vcodes.data = other[1].cpu()
+    with pytest.raises(ValueError, match="any more"):
+        cache.had_cache_read(f.cache, f.table, ints([0]), 1)
