@@ -426,8 +426,8 @@ typedef struct {
  * minimum rounded down to bf16, s = fl(fl(max - z) / 15) rounded up to bf16,
  * c = fl(fl(v - z) / s) rounded to the nearest whole number, ties to even,
  * clamped to [0, 15]; s = 0 gives c = 0.  |c s + z - v| <= s / 2 plus fp32
- * rounding.  A row with a NaN or an infinity, or whose z or 15 s is not
- * finite, gets s = z = NaN.  The pages have to be there and the sequence's own
+ * rounding.  A row with a NaN or an infinity, or whose z, 15 s or fl(15 s + z)
+ * is not finite, gets s = z = NaN.  The pages have to be there and the sequence's own
  * (had_cache_reserve); places behind the written tokens are left as they were.
  */
 HAD_API had_status_t had_cache_append(const void *K, const void *V, had_dtype_t dt,

@@ -27,6 +27,8 @@ def quantise(v):
         zero = bf16_round(v.min(-1) + np.float32(0), -1)
         scale = bf16_round((v.max(-1) - zero) / np.float32(15), +1)
         fine = np.isfinite(v).all(-1) & np.isfinite(zero) & np.isfinite(np.float32(15) * scale)
+        most = 15 * scale.astype(np.float64) + zero                # exact, then rounded once
+        fine &= np.isfinite(most.astype(np.float32))
         step = np.where(fine & (scale > 0), scale, np.float32(1))[..., None]
         code = np.clip(np.rint((v - zero[..., None]) / step), 0, 15)
         code = np.where((fine & (scale > 0))[..., None], code, 0)

@@ -216,8 +216,8 @@ struct CacheSlice {
 // nearest whole number (even on ties); s and z are rounded outwards, so a
 // quotient lies in [0, 15 (1 + 2^-23)] and needs no clamp.  s = 0 (a constant
 // row that bf16 holds) gives codes 0.  A row with a NaN or an infinity, or
-// whose z or 15 s is not finite, gets s = z = NaN and codes 0: whoever keeps
-// it sees NaN.
+// whose z, 15 s or 15 s + z is not finite, gets s = z = NaN and codes 0: whoever
+// keeps it sees NaN.
 //
 // HBM-bound once the arithmetic is lean: 2 d elements read, d/8 + d/2 + 4
 // bytes written per row.  4 lanes take a row: what a row costs once (place,
@@ -287,7 +287,7 @@ cache_append_kernel(const T *__restrict__ K, const T *__restrict__ V,
         const float z = bf16_down(lo + 0.0f);         // -0 becomes +0
         const float s = -bf16_down(-__fdiv_rn(hi - z, 15.0f)) + 0.0f;
         const bool fine = fabsf(lo) <= FLT_MAX && fabsf(hi) <= FLT_MAX && fabsf(z) <= FLT_MAX &&
-                          15.0f * s <= FLT_MAX;
+                          15.0f * s <= FLT_MAX && fmaf(15.0f, s, z) <= FLT_MAX;
         const bool coded = fine && s > 0.0f;
         const float inv = __frcp_rn(s);
         // four codes c0 + 16 c1 + 256 c2 + 4096 c3 are a whole number below

@@ -1233,3 +1233,25 @@ def test_a_cache_whose_tensors_get_other_storage(cache):
     f.cache.vcodes.data = other[1].cpu()
     with pytest.raises(ValueError, match="any more"):
         cache.had_cache_read(f.cache, f.table, ints([0]), 1)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_whose_largest_code_would_overflow(cache, dtype, d):
+    """Rows up to the largest number of bf16, where 15 s + z may pass fp32: marked, never infinite."""
+    T, most = 256, torch.finfo(BF16).max
+    g = torch.Generator().manual_seed(d)
+    low = most * 10.0 ** torch.linspace(-3, 0, T, dtype=torch.float64)[:, None]
+    v = low + (most - low) * torch.rand(1, 1, T, d, generator=g, dtype=torch.float64)
+    v[..., 3], v[..., 5] = most, low[:, 0]
+    v = v.clamp(max=most).to(dtype)
+    c = cache.Cache.empty(1, 1, 256, d)
+    st = status()
+    cache.had_cache_append(v.cuda(), v.cuda(), torch.ones(1, device="cuda"), c, ints([[0]]), ints([0]),
+                           dev_status=st)
+    values = cache.had_cache_read(c, ints([[0]]), ints([0]), T, dev_status=st)[1].cpu().numpy()
+    code, s, z = ocache.quantise(v.float().numpy())
+    assert 0 < np.isnan(s).sum() < T and not np.isinf(values).any()
+    exact = (code * s[..., None].astype(np.float64) + z[..., None]).astype(np.float32)
+    assert np.array_equal(values, exact, equal_nan=True)
+    assert flags(st) == 0

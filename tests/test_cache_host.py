@@ -334,3 +334,11 @@ def test_books_by_hand_where_entries_are_missing_behind_the_length():
     b.lens = [0]
     assert b.reserve([80]) == ([-1], [-1])
     assert b.table == [[0, 1, 4, 3, 2]] and b.refs == [1, 1, 1, 1, 1, 0, 0]
+
+
+def test_quantise_marks_rows_whose_largest_code_would_overflow():
+    v = np.full((3, 64), 3.30e38, np.float32)
+    v[:, 0] = 3.4028235e38, 3.35e38, 3.30e38
+    c, s, z = ocache.quantise(v)
+    assert np.isnan(s[0]) and np.isnan(z[0]) and not c[0].any()
+    assert np.isfinite(s[1:]).all() and np.isfinite(c[1:] * s[1:, None] + z[1:, None]).all()
