@@ -166,7 +166,8 @@ def had_cache_fork(table, lens, refs, page, src, dst, dev_status=None, stream=No
 def had_cache_reserve(table, lens, refs, page, grow, src=None, dst=None, dev_status=None,
                       stream=None):
     """Room for grow[s] more tokens of every sequence, in place; returns (src [S], dst [S]) int32,
-    the shared last pages to be copied (-1: none) with had_cache_copy_pages."""
+    the shared last pages to be copied (-1: none) with had_cache_copy_pages.  lens may have gone
+    back since the last call: pages behind it are kept unless another sequence names them too."""
     return _call(_native.reserve, "had_cache_reserve",
                  (table, lens, refs, page, grow, src, dst, dev_status), stream, table)
 

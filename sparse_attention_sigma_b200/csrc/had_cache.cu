@@ -164,7 +164,7 @@ had_status_t launch_attention_tile(const had::CacheAttnArgs &a, int B, int max_l
     // 1028 22.5, 21.5, 31, 58 us; one of 128 keys 6.4, 7.7, 7.4, 8.0 us.  More
     // CTAs, until their memory holds a tile's keys whole, only for as many keys as
     // the caller says there are: keys that do not fit are gone through twice (1024
-    // tiles of 16 k keys 608 us instead of 428), but a table is often wider than
+    // tiles of 16 k keys 620 us instead of 426), but a table is often wider than
     // its sequences, and a cluster keeps its places until its last CTA is done (512
     // tiles of 4 k keys in a table for 128 k: 71 us, with 4 CTAs 94, with 8 149 us).
     const long long expected = max_len < keys ? max_len : keys;

@@ -37,10 +37,10 @@
 //
 // mma.sync and not tcgen05: a tile has 4 or 8 rows of 64 or 128, B is made in
 // registers from gathered codes, and the tensor pipe is 10 % busy.  What bounds
-// it is the issue of the instructions around the product (16 sequences of 16 k
-// tokens, 32 query and 8 key heads, d 128, N 2048: 68 us, 31 M warp
-// instructions, half of all issue slots; 127 MB from memory would take 19 us):
-// about 20 a (row, 32 keys) for distances and selection, 300 per 16 kept keys
+// it is the instructions around the product and their latency at 16 warps an SM
+// (16 sequences of 16 k tokens, 32 query and 8 key heads, d 128, N 2048: 67 us,
+// 31 M warp instructions in half of the issue slots; 127 MB from memory would
+// take 19 us): about 20 a (row, 32 keys) for distances and selection, 300 per 16 kept keys
 // of d 128, of which 100 unpack and multiply codes, 70 make the weights and 40
 // copy.  The accumulators' registers allow 16 warps an SM at d 128 and 20 to 24
 // at 64; more spill (20 and 24 at d 128, with the bf16 form of step 4: 95 and
